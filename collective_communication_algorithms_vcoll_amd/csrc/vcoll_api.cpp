@@ -13,6 +13,7 @@
 #include "reduce.h"
 #include "step.h"
 #include "schedule.h"
+#include "validate.h"
 #include "vcoll.h"
 #include "vcoll_bench.h"
 
@@ -20,46 +21,12 @@ using namespace vcoll;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-thread_local const char* g_last_hip_error = "";
-
-vcoll_status from_hip(hipError_t e) {
-  if (e == hipSuccess) return VCOLL_OK;
-  g_last_hip_error = hipGetErrorString(e);
-  return VCOLL_ERR_HIP;
-}
-
-int64_t elem_bytes(vcoll_dtype d) { return d == VCOLL_F32 ? 4 : (d == VCOLL_BF16 ? 2 : 1); }
-
-bool valid_dtype(int d) { return d == VCOLL_F32 || d == VCOLL_BF16; }
-
-// the all-to-all only moves rows, so it also takes raw bytes
-bool valid_a2a_dtype(int d) { return valid_dtype(d) || d == VCOLL_U8; }
-
 bool valid_algo(int a) { return a >= VCOLL_RING && a <= VCOLL_BINARY_TREE; }
-
-bool valid_p(int p) { return p >= 1 && p <= kMaxRanks; }
 
 // nodes x local ranks: each factor is bounded before the product is formed,
 // so the product cannot overflow int
 bool valid_grid(int nodes, int local) {
   return nodes >= 1 && local >= 1 && nodes <= kMaxRanks && local <= kMaxRanks && valid_p(nodes * local);
-}
-
-// rows x topk within int32 (the row indices of the MoE maps), tested by
-// division so that the product is only formed once it is known to fit
-bool pairs_fit(int64_t rows, int topk) { return topk >= 1 && rows >= 0 && rows <= INT32_MAX / topk; }
-
-// Element counts up to 2^48: far beyond any buffer, and small enough that
-// every byte offset (count x 4 bytes x up to 128 ranks) fits in int64.
-constexpr int64_t kMaxCount = int64_t(1) << 48;
-
-bool valid_count(int64_t n) { return n >= 0 && n <= kMaxCount; }
-
-// A buffer of `rows` rows of `row_bytes` bytes stays within 2^56 bytes.
-bool fits(int64_t rows, int64_t row_bytes) {
-  return row_bytes <= 0 || rows <= (int64_t(1) << 56) / row_bytes;
 }
 
 // Row counts of an all-to-all: every entry >= 0 and each rank's sent and
@@ -79,19 +46,6 @@ bool valid_splits(int p, const int64_t* splits, int64_t row_bytes, std::vector<i
     }
   for (int i = 0; i < p; ++i)
     if (!fits(sent[i], row_bytes) || !fits(got[i], row_bytes)) return false;
-  return true;
-}
-
-bool all_set(int p, const void* const* ptrs) {
-  if (!ptrs) return false;
-  for (int r = 0; r < p; ++r)
-    if (!ptrs[r]) return false;
-  return true;
-}
-
-bool all_aligned(int p, const void* const* ptrs) {
-  for (int r = 0; r < p; ++r)
-    if (!aligned16(ptrs[r])) return false;
   return true;
 }
 
