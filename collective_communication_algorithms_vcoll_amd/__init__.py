@@ -1042,3 +1042,9 @@ def prepare_allreduce_stepwise(algo, send, recv, workspace=None) -> PreparedCall
     args = (_algo(algo), len(s), n, _dtype_code(s[0]), sp, rp, ws_ptr, ws_bytes, None, _stream(s[0]))
     return PreparedCall("vcoll_allreduce_stepwise", _lib().vcoll_allreduce_stepwise, args,
                         (send, recv, workspace, sp, rp))
+
+
+# the training-step operators, under the same names as in vcoll.h
+from .training import (AdamwStep, adamw_state, prepare_adamw, vcoll_adamw, vcoll_adamw_unpack,  # noqa: E402,F401
+                       vcoll_moe_combine_weighted, vcoll_moe_combine_weighted_backward, vcoll_moe_route,
+                       vcoll_moe_route_backward, vcoll_moe_sort, vcoll_moe_sort_workspace)

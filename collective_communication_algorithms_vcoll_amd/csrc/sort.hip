@@ -1,0 +1,156 @@
+// Stable counting sort of (rank, token, slot) pairs by expert id. A pair's
+// place in its expert's run is the number of earlier pairs with the same
+// expert; the runs of the experts of one rank follow each other in that
+// rank's receive buffer.
+//
+// Pairs are cut into tiles, one workgroup each, and a tile into one run of
+// pairs per wave. With several tiles a first launch counts every tile's
+// pairs per expert and the second adds up the counts of the tiles before its
+// own; one tile needs one launch. Inside a wave, the 64 pairs of a step find
+// the earlier lanes with their expert by one ballot per bit of the id.
+#include "device.h"
+#include "train.h"
+
+namespace vcoll {
+namespace {
+
+using namespace dev;
+
+constexpr int kSortBlock = 1024;
+constexpr int kSortWaves = kSortBlock / 64;
+
+// Expert of pair n, or -1 for a pair without one.
+__device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t n) {
+  const uint32_t i = n / static_cast<uint32_t>(a.pairs_per_rank);
+  const int e = a.ids[i][n - i * a.pairs_per_rank];
+  return e >= 0 && e < a.experts ? e : -1;
+}
+
+// Counts the pairs of this workgroup's tile per wave and expert into
+// count[kSortWaves][experts].
+__device__ __forceinline__ void count_tile(const SortArgs& a, int32_t* count, uint32_t begin, uint32_t end) {
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  for (int x = threadIdx.x; x < kSortWaves * a.experts; x += kSortBlock) count[x] = 0;
+  __syncthreads();
+  const uint32_t run = a.tile / kSortWaves;
+  for (uint32_t s = 0; s < run; s += 64) {
+    const uint32_t n = begin + wave * run + s + lane;
+    const int e = n < end ? expert_of(a, n) : -1;
+    if (e >= 0) atomicAdd(&count[wave * a.experts + e], 1);
+  }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kSortBlock) void sort_count_kernel(const SortArgs a) {
+  extern __shared__ int32_t count[];
+  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(a.tile);
+  const uint32_t end = min(begin + static_cast<uint32_t>(a.tile), static_cast<uint32_t>(a.pairs));
+  count_tile(a, count, begin, end);
+  for (int e = threadIdx.x; e < a.experts; e += kSortBlock) {
+    int32_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) sum += count[w * a.experts + e];
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + e] = sum;
+  }
+}
+
+__global__ __launch_bounds__(kSortBlock) void sort_place_kernel(const SortArgs a) {
+  extern __shared__ int32_t next[];                       // [kSortWaves][experts]
+  __shared__ int32_t scan[kSortBlock + 1];                // pairs of all experts before e
+  __shared__ int32_t wave_total[kSortWaves];
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(a.tile);
+  const uint32_t end = min(begin + static_cast<uint32_t>(a.tile), static_cast<uint32_t>(a.pairs));
+  count_tile(a, next, begin, end);
+
+  // thread e: pairs of expert e in all tiles, and in the tiles before this one
+  int32_t total = 0, before = 0;
+  if (tid < a.experts) {
+    if (a.blocks == 1) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) total += next[w * a.experts + tid];
+    } else {
+#pragma unroll 8
+      for (int b = 0; b < a.blocks; ++b) {
+        const int32_t c = a.counts[static_cast<int64_t>(b) * a.experts + tid];
+        total += c;
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+    }
+  }
+  int32_t sum = total;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t x = __shfl_up(sum, d);
+    if (lane >= d) sum += x;
+  }
+  if (lane == 63) wave_total[wave] = sum;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) sum += wave_total[w];
+  scan[tid + 1] = sum;
+  if (tid == 0) scan[0] = 0;
+  __syncthreads();
+  if (tid < a.experts) {
+    const int j = tid / a.experts_per_rank;
+    const int32_t first = scan[tid] - scan[j * a.experts_per_rank];
+    int32_t at = first + before;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int32_t c = next[w * a.experts + tid];
+      next[w * a.experts + tid] = at;
+      at += c;
+    }
+    if (blockIdx.x == 0) {
+      int32_t* row = a.offsets + static_cast<int64_t>(j) * (a.experts_per_rank + 1);
+      row[tid - j * a.experts_per_rank] = first;
+      if (tid + 1 == (j + 1) * a.experts_per_rank) row[a.experts_per_rank] = first + total;
+    }
+  }
+  __syncthreads();
+
+  const uint32_t run = a.tile / kSortWaves;
+  for (uint32_t s = 0; s < run; s += 64) {
+    const uint32_t n = begin + wave * run + s + lane;
+    const int e = n < end ? expert_of(a, n) : -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int bit = 1; bit < a.experts; bit <<= 1) {
+      const uint64_t ones = __ballot((e & bit) != 0);
+      same &= (e & bit) ? ones : ~ones;
+    }
+    int32_t row = -1, rank = -1;
+    const int leader = e >= 0 ? __ffsll(static_cast<unsigned long long>(same)) - 1 : lane;
+    int32_t at = 0;
+    if (e >= 0 && lane == leader) at = atomicAdd(&next[wave * a.experts + e], __popcll(same));
+    at = __shfl(at, leader);
+    if (e >= 0) {
+      rank = e / a.experts_per_rank;
+      row = at + __popcll(same & ((uint64_t(1) << lane) - 1));
+    }
+    if (n < end) {
+      const uint32_t i = n / static_cast<uint32_t>(a.pairs_per_rank);
+      int32_t* slot = a.slots[i] + 2 * static_cast<int64_t>(n - i * a.pairs_per_rank);
+      slot[0] = rank;
+      slot[1] = row;
+    }
+  }
+}
+
+template <class K>
+hipError_t launch_lds(K kernel, int blocks, size_t lds, const SortArgs& a, hipStream_t stream) {
+  void* args[] = {const_cast<SortArgs*>(&a)};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(blocks), dim3(kSortBlock), args, lds, stream);
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
+  static_assert(kMaxExperts <= kSortBlock, "one thread per expert");
+  const size_t lds = static_cast<size_t>(kSortWaves) * a.experts * sizeof(int32_t);   // at most 64 KiB
+  if (a.blocks > 1) {
+    const hipError_t e = launch_lds(sort_count_kernel, a.blocks, lds, a, stream);
+    if (e != hipSuccess) return e;
+  }
+  return launch_lds(sort_place_kernel, a.blocks, lds, a, stream);
+}
+
+}  // namespace vcoll

@@ -1,0 +1,142 @@
+// Launch interface of the training-step kernels: the MoE router and its
+// gradient (route.hip), the expert sort (sort.hip), the weighted combine and
+// its gradient (weighted.hip) and the AdamW step (adamw.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "common.h"
+#include "vcoll.h"
+
+namespace vcoll {
+
+// Token-owning ranks described per launch (kernel arguments are limited to
+// 4 KiB); more ranks take further launches.
+constexpr int kTokenRanks = 32;
+
+constexpr int kMaxExperts = 1024;    // experts of one router or sort: one thread, or 16 per lane, each
+constexpr int kMaxTopk = 64;         // chosen experts per token: one lane each
+
+// Grid: x = token tiles, y = rank.
+struct RouteArgs {
+  const void* logits[kTokenRanks];   // [tokens][experts]
+  int32_t* ids[kTokenRanks];         // [tokens][topk]
+  float* weights[kTokenRanks];       // [tokens][topk]
+  int64_t tokens;
+  int32_t experts, topk, normalise;
+  int32_t ranks;                     // ranks of this launch
+};
+
+struct RouteBackwardArgs {
+  const void* logits[kTokenRanks];
+  const int32_t* ids[kTokenRanks];
+  const float* weights[kTokenRanks];
+  const float* d_weights[kTokenRanks];
+  void* d_logits[kTokenRanks];       // [tokens][experts]
+  int64_t tokens;
+  int32_t experts, topk, normalise;
+  int32_t ranks;
+};
+
+// Pairs in (rank, token, slot) order are cut into `blocks` tiles of `tile`.
+struct SortArgs {
+  const int32_t* ids[kMaxRanks];     // [pairs_per_rank]
+  int32_t* slots[kMaxRanks];         // [pairs_per_rank][2]
+  int32_t* offsets;                  // [p][experts_per_rank + 1]
+  int32_t* counts;                   // [blocks][experts] (workspace; unused with one block)
+  int32_t p, experts, experts_per_rank;
+  int32_t pairs_per_rank;
+  int32_t pairs;                     // p * pairs_per_rank
+  int32_t tile, blocks;
+};
+static_assert(sizeof(SortArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+struct WeightedArgs {
+  const void* expert_out[kMaxRanks];
+  int32_t expert_rows[kMaxRanks];
+  const int32_t* slots[kTokenRanks];   // [tokens * topk][2]
+  const float* weights[kTokenRanks];   // [tokens * topk], null: ones
+  void* out[kTokenRanks];              // [tokens][hidden]
+  int64_t tokens, hidden;
+  int32_t topk, p;
+  int32_t vec;                         // rows and bases 16-byte aligned
+  int32_t ranks;
+};
+static_assert(sizeof(WeightedArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+struct WeightedBackwardArgs {
+  const void* expert_out[kMaxRanks];
+  void* d_expert_out[kMaxRanks];
+  int32_t expert_rows[kMaxRanks];
+  const void* d_out[kTokenRanks];      // [tokens][hidden]
+  const int32_t* slots[kTokenRanks];
+  const float* weights[kTokenRanks];
+  float* d_weights[kTokenRanks];       // [tokens * topk]
+  int64_t tokens, hidden;
+  int32_t topk, p;
+  int32_t vec;
+  int32_t ranks;
+};
+static_assert(sizeof(WeightedBackwardArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+constexpr int kAdamwTensors = 48;    // tensors described per launch
+constexpr int kAdamwGroup = 128;     // elements per scale of an 8-bit state
+constexpr int kAdamwTile = 2048;     // elements per workgroup, a multiple of the group
+
+struct AdamwTensor {
+  int64_t n;
+  void* param;
+  const void* grad;
+  float* master;                     // null with float32 parameters
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;              // null with float32 states
+  float* exp_avg_sq_scale;
+  int32_t tile_start;                // first workgroup of this tensor
+  uint32_t key;                      // of the tensor's random rounding
+};
+
+struct AdamwArgs {
+  AdamwTensor t[kAdamwTensors];
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float grad_scale;
+  float decay;                       // 1 - lr * weight_decay
+  float step_size;                   // lr / (1 - beta1^step)
+  float root_bc2;                    // 1 / sqrt(1 - beta2^step)
+  float eps;
+  int32_t count;
+};
+static_assert(sizeof(AdamwArgs) <= 4096, "kernel arguments are limited to 4 KiB");
+
+struct UnpackArgs {
+  const uint8_t* exp_avg;
+  const uint8_t* exp_avg_sq;
+  const float* exp_avg_scale;
+  const float* exp_avg_sq_scale;
+  float* exp_avg_out;
+  float* exp_avg_sq_out;
+  int64_t n;
+};
+
+hipError_t launch_route(const RouteArgs& a, vcoll_dtype dtype, hipStream_t stream);
+hipError_t launch_route_backward(const RouteBackwardArgs& a, vcoll_dtype dtype, hipStream_t stream);
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream);
+hipError_t launch_weighted(const WeightedArgs& a, vcoll_dtype dtype, hipStream_t stream);
+hipError_t launch_weighted_backward(const WeightedBackwardArgs& a, vcoll_dtype dtype, hipStream_t stream);
+hipError_t launch_adamw(const AdamwArgs& a, int32_t tiles, vcoll_dtype param, vcoll_dtype grad, int state_bits,
+                        hipStream_t stream);
+hipError_t launch_unpack(const UnpackArgs& a, hipStream_t stream);
+
+// The 32-bit mixing that random rounding draws from: two rounds of xor-shift
+// and multiplication by an odd constant, a bijection of its argument.
+__host__ __device__ inline uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0x85157AF5u;
+  return x ^ (x >> 16);
+}
+
+}  // namespace vcoll

@@ -1,0 +1,346 @@
+// C entry points of the training-step operators: validation, launch
+// descriptors, dispatch. Every check happens before the first launch.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "train.h"
+#include "validate.h"
+#include "vcoll.h"
+
+using namespace vcoll;
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool aligned_to(const void* p, vcoll_dtype d) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(d) == 0; }
+
+template <class T>
+bool all_given(int p, T* const* ptrs) {
+  return all_set(p, reinterpret_cast<const void* const*>(ptrs));
+}
+
+bool valid_router(int p, int64_t tokens, int experts, int topk, int dtype) {
+  return valid_p(p) && valid_count(tokens) && experts >= 1 && topk >= 1 && topk <= experts && valid_dtype(dtype) &&
+         pairs_fit(tokens, topk) && fits(tokens, static_cast<int64_t>(experts) * 4);
+}
+
+// x workgroups of up to 1024 threads each stay within 2^32 threads of a grid dimension
+bool grid_fits(int64_t groups) { return groups <= (int64_t(UINT32_MAX) >> 10); }
+
+// Calls run(first rank, ranks) for groups of at most kTokenRanks ranks.
+template <class F>
+vcoll_status by_ranks(int p, F&& run) {
+  for (int i0 = 0; i0 < p; i0 += kTokenRanks) {
+    const vcoll_status st = run(i0, std::min(kTokenRanks, p - i0));
+    if (st != VCOLL_OK) return st;
+  }
+  return VCOLL_OK;
+}
+
+// Tiles of the expert sort: at most kSortTiles, each a whole number of steps
+// of its 16 waves.
+constexpr int64_t kSortStep = 1024;
+constexpr int64_t kSortTiles = 256;
+
+int64_t sort_tile(int64_t pairs) {
+  const int64_t per = (pairs + kSortTiles - 1) / kSortTiles;
+  return std::max<int64_t>(1, (per + kSortStep - 1) / kSortStep) * kSortStep;
+}
+
+bool valid_sort(int p, int64_t tokens, int topk, int experts_per_rank) {
+  return valid_p(p) && valid_count(tokens) && topk >= 1 && experts_per_rank >= 1 && pairs_fit(tokens, topk) &&
+         tokens * topk <= INT32_MAX / p;
+}
+
+int64_t sort_blocks(int64_t pairs) { return std::max<int64_t>(1, (pairs + sort_tile(pairs) - 1) / sort_tile(pairs)); }
+
+int64_t sort_bytes(int64_t pairs, int64_t experts) {
+  const int64_t blocks = sort_blocks(pairs);
+  return blocks > 1 ? blocks * experts * 4 : 0;
+}
+
+vcoll_status check_rows(int p, int64_t tokens, int topk, int64_t hidden, int dtype, const int64_t* expert_rows) {
+  if (!valid_p(p) || !valid_count(tokens) || topk < 1 || !valid_count(hidden) || !valid_dtype(dtype) || !expert_rows)
+    return VCOLL_ERR_INVALID_ARG;
+  if (!pairs_fit(tokens, topk) || hidden > INT32_MAX / 4) return VCOLL_ERR_INVALID_ARG;
+  const int64_t rb = hidden * elem_bytes(static_cast<vcoll_dtype>(dtype));
+  if (!fits(tokens, rb)) return VCOLL_ERR_INVALID_ARG;
+  for (int j = 0; j < p; ++j)
+    if (expert_rows[j] < 0 || expert_rows[j] > INT32_MAX || !fits(expert_rows[j], rb)) return VCOLL_ERR_INVALID_ARG;
+  return grid_fits(tokens) ? VCOLL_OK : VCOLL_ERR_UNSUPPORTED;
+}
+
+bool valid_hyper(const vcoll_adamw_hyper* h) {
+  return h && std::isfinite(h->lr) && h->lr >= 0 && h->beta1 >= 0 && h->beta1 < 1 && h->beta2 >= 0 && h->beta2 < 1 &&
+         std::isfinite(h->eps) && h->eps >= 0 && std::isfinite(h->weight_decay) && h->weight_decay >= 0 &&
+         std::isfinite(h->grad_scale) && h->step >= 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+vcoll_status vcoll_moe_route(int p, int64_t tokens, int experts, int topk, vcoll_dtype dtype, int normalise,
+                             const void* const* logits, int32_t* const* ids, float* const* weights, void* stream) {
+  if (!valid_router(p, tokens, experts, topk, dtype)) return VCOLL_ERR_INVALID_ARG;
+  if (experts > kMaxExperts || topk > kMaxTopk || !grid_fits(tokens)) return VCOLL_ERR_UNSUPPORTED;
+  if (tokens == 0) return VCOLL_OK;
+  if (!all_set(p, logits) || !all_given(p, ids) || !all_given(p, weights)) return VCOLL_ERR_INVALID_ARG;
+  for (int i = 0; i < p; ++i)
+    if (!aligned_to(logits[i], dtype) || !aligned4(ids[i]) || !aligned4(weights[i])) return VCOLL_ERR_INVALID_ARG;
+  return by_ranks(p, [&](int i0, int n) {
+    RouteArgs a;
+    std::memset(&a, 0, sizeof(a));
+    for (int i = 0; i < n; ++i) {
+      a.logits[i] = logits[i0 + i];
+      a.ids[i] = ids[i0 + i];
+      a.weights[i] = weights[i0 + i];
+    }
+    a.tokens = tokens;
+    a.experts = experts;
+    a.topk = topk;
+    a.normalise = normalise != 0;
+    a.ranks = n;
+    return from_hip(launch_route(a, dtype, static_cast<hipStream_t>(stream)));
+  });
+}
+
+vcoll_status vcoll_moe_route_backward(int p, int64_t tokens, int experts, int topk, vcoll_dtype dtype, int normalise,
+                                      const void* const* logits, const int32_t* const* ids,
+                                      const float* const* weights, const float* const* d_weights,
+                                      void* const* d_logits, void* stream) {
+  if (!valid_router(p, tokens, experts, topk, dtype)) return VCOLL_ERR_INVALID_ARG;
+  if (experts > kMaxExperts || topk > kMaxTopk || !grid_fits(tokens)) return VCOLL_ERR_UNSUPPORTED;
+  if (tokens == 0) return VCOLL_OK;
+  if ((!normalise && !all_set(p, logits)) || !all_given(p, ids) || !all_given(p, weights) || !all_given(p, d_weights) ||
+      !all_given(p, d_logits))
+    return VCOLL_ERR_INVALID_ARG;
+  for (int i = 0; i < p; ++i)
+    if ((!normalise && !aligned_to(logits[i], dtype)) || !aligned4(ids[i]) || !aligned4(weights[i]) ||
+        !aligned4(d_weights[i]) || !aligned_to(d_logits[i], dtype))
+      return VCOLL_ERR_INVALID_ARG;
+  return by_ranks(p, [&](int i0, int n) {
+    RouteBackwardArgs a;
+    std::memset(&a, 0, sizeof(a));
+    for (int i = 0; i < n; ++i) {
+      a.logits[i] = normalise ? nullptr : logits[i0 + i];
+      a.ids[i] = ids[i0 + i];
+      a.weights[i] = weights[i0 + i];
+      a.d_weights[i] = d_weights[i0 + i];
+      a.d_logits[i] = d_logits[i0 + i];
+    }
+    a.tokens = tokens;
+    a.experts = experts;
+    a.topk = topk;
+    a.normalise = normalise != 0;
+    a.ranks = n;
+    return from_hip(launch_route_backward(a, dtype, static_cast<hipStream_t>(stream)));
+  });
+}
+
+vcoll_status vcoll_moe_sort_workspace(int p, int64_t tokens, int topk, int experts_per_rank, int64_t* bytes) {
+  if (!bytes || !valid_sort(p, tokens, topk, experts_per_rank)) return VCOLL_ERR_INVALID_ARG;
+  if (experts_per_rank > kMaxExperts / p) return VCOLL_ERR_UNSUPPORTED;
+  *bytes = sort_bytes(p * tokens * topk, static_cast<int64_t>(p) * experts_per_rank);
+  return VCOLL_OK;
+}
+
+vcoll_status vcoll_moe_sort(int p, int64_t tokens, int topk, int experts_per_rank, const int32_t* const* ids,
+                            int32_t* const* slots, int32_t* offsets, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+  if (!valid_sort(p, tokens, topk, experts_per_rank)) return VCOLL_ERR_INVALID_ARG;
+  if (experts_per_rank > kMaxExperts / p) return VCOLL_ERR_UNSUPPORTED;
+  const int64_t pairs = p * tokens * topk;
+  const int64_t need = sort_bytes(pairs, static_cast<int64_t>(p) * experts_per_rank);
+  if (!offsets || !aligned4(offsets)) return VCOLL_ERR_INVALID_ARG;
+  if (tokens > 0 && (!all_given(p, ids) || !all_given(p, slots))) return VCOLL_ERR_INVALID_ARG;
+  for (int i = 0; tokens > 0 && i < p; ++i)
+    if (!aligned4(ids[i]) || (reinterpret_cast<uintptr_t>(slots[i]) & 7u) != 0) return VCOLL_ERR_INVALID_ARG;
+  if (need > 0) {
+    if (workspace_bytes < need) return VCOLL_ERR_BUFFER_TOO_SMALL;
+    if (!workspace || !aligned4(workspace)) return VCOLL_ERR_INVALID_ARG;
+  }
+  SortArgs a;
+  std::memset(&a, 0, sizeof(a));
+  for (int i = 0; tokens > 0 && i < p; ++i) {
+    a.ids[i] = ids[i];
+    a.slots[i] = slots[i];
+  }
+  a.offsets = offsets;
+  a.counts = static_cast<int32_t*>(workspace);
+  a.p = p;
+  a.experts_per_rank = experts_per_rank;
+  a.experts = p * experts_per_rank;
+  a.pairs_per_rank = static_cast<int32_t>(tokens * topk);
+  a.pairs = static_cast<int32_t>(pairs);
+  a.tile = static_cast<int32_t>(sort_tile(pairs));
+  a.blocks = static_cast<int32_t>(sort_blocks(pairs));
+  return from_hip(launch_sort(a, static_cast<hipStream_t>(stream)));
+}
+
+vcoll_status vcoll_moe_combine_weighted(int p, int64_t tokens, int topk, int64_t hidden, vcoll_dtype dtype,
+                                        const void* const* expert_out, const int64_t* expert_rows,
+                                        const int32_t* const* slots, const float* const* weights, void* const* out,
+                                        void* stream) {
+  const vcoll_status st = check_rows(p, tokens, topk, hidden, dtype, expert_rows);
+  if (st != VCOLL_OK) return st;
+  if (tokens == 0 || hidden == 0) return VCOLL_OK;
+  if (!expert_out || !all_given(p, slots) || !all_set(p, out) || (weights && !all_given(p, weights)))
+    return VCOLL_ERR_INVALID_ARG;
+  bool vec = hidden * elem_bytes(dtype) % 16 == 0;
+  for (int j = 0; j < p; ++j) {
+    if (expert_rows[j] > 0 && (!expert_out[j] || !aligned_to(expert_out[j], dtype))) return VCOLL_ERR_INVALID_ARG;
+    if (!aligned_to(out[j], dtype) || !aligned4(slots[j]) || (weights && !aligned4(weights[j])))
+      return VCOLL_ERR_INVALID_ARG;
+    vec = vec && aligned16(out[j]) && (expert_rows[j] == 0 || aligned16(expert_out[j]));
+  }
+  return by_ranks(p, [&](int i0, int n) {
+    WeightedArgs a;
+    std::memset(&a, 0, sizeof(a));
+    for (int j = 0; j < p; ++j) {
+      a.expert_out[j] = expert_out[j];
+      a.expert_rows[j] = static_cast<int32_t>(expert_rows[j]);
+    }
+    for (int i = 0; i < n; ++i) {
+      a.slots[i] = slots[i0 + i];
+      a.weights[i] = weights ? weights[i0 + i] : nullptr;
+      a.out[i] = out[i0 + i];
+    }
+    a.tokens = tokens;
+    a.hidden = hidden;
+    a.topk = topk;
+    a.p = p;
+    a.vec = vec;
+    a.ranks = n;
+    return from_hip(launch_weighted(a, dtype, static_cast<hipStream_t>(stream)));
+  });
+}
+
+vcoll_status vcoll_moe_combine_weighted_backward(int p, int64_t tokens, int topk, int64_t hidden, vcoll_dtype dtype,
+                                                 const void* const* d_out, const void* const* expert_out,
+                                                 const int64_t* expert_rows, const int32_t* const* slots,
+                                                 const float* const* weights, void* const* d_expert_out,
+                                                 float* const* d_weights, void* stream) {
+  const vcoll_status st = check_rows(p, tokens, topk, hidden, dtype, expert_rows);
+  if (st != VCOLL_OK) return st;
+  if (hidden == 0) return VCOLL_ERR_INVALID_ARG;
+  if (tokens == 0) return VCOLL_OK;
+  if (!expert_out || !d_expert_out || !all_given(p, slots) || !all_given(p, weights) || !all_given(p, d_weights) ||
+      !all_set(p, d_out))
+    return VCOLL_ERR_INVALID_ARG;
+  bool vec = hidden * elem_bytes(dtype) % 16 == 0;
+  for (int j = 0; j < p; ++j) {
+    const bool rows = expert_rows[j] > 0;
+    if (rows && (!expert_out[j] || !d_expert_out[j] || !aligned_to(expert_out[j], dtype) ||
+                 !aligned_to(d_expert_out[j], dtype)))
+      return VCOLL_ERR_INVALID_ARG;
+    if (!aligned_to(d_out[j], dtype) || !aligned4(slots[j]) || !aligned4(weights[j]) || !aligned4(d_weights[j]))
+      return VCOLL_ERR_INVALID_ARG;
+    vec = vec && aligned16(d_out[j]) && (!rows || (aligned16(expert_out[j]) && aligned16(d_expert_out[j])));
+  }
+  return by_ranks(p, [&](int i0, int n) {
+    WeightedBackwardArgs a;
+    std::memset(&a, 0, sizeof(a));
+    for (int j = 0; j < p; ++j) {
+      a.expert_out[j] = expert_out[j];
+      a.d_expert_out[j] = d_expert_out[j];
+      a.expert_rows[j] = static_cast<int32_t>(expert_rows[j]);
+    }
+    for (int i = 0; i < n; ++i) {
+      a.d_out[i] = d_out[i0 + i];
+      a.slots[i] = slots[i0 + i];
+      a.weights[i] = weights[i0 + i];
+      a.d_weights[i] = d_weights[i0 + i];
+    }
+    a.tokens = tokens;
+    a.hidden = hidden;
+    a.topk = topk;
+    a.p = p;
+    a.vec = vec;
+    a.ranks = n;
+    return from_hip(launch_weighted_backward(a, dtype, static_cast<hipStream_t>(stream)));
+  });
+}
+
+vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dtype param_dtype, vcoll_dtype grad_dtype,
+                         int state_bits, const vcoll_adamw_hyper* hyper, void* stream) {
+  if (count < 0 || !valid_dtype(param_dtype) || !valid_dtype(grad_dtype) || (state_bits != 32 && state_bits != 8) ||
+      !valid_hyper(hyper) || (count > 0 && !tensors))
+    return VCOLL_ERR_INVALID_ARG;
+  const vcoll_dtype state = state_bits == 32 ? VCOLL_F32 : VCOLL_U8;
+  for (int k = 0; k < count; ++k) {
+    const vcoll_adamw_tensor& t = tensors[k];
+    if (!valid_count(t.n)) return VCOLL_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || !aligned_to(t.param, param_dtype) ||
+        !aligned_to(t.grad, grad_dtype) || !aligned_to(t.exp_avg, state) || !aligned_to(t.exp_avg_sq, state))
+      return VCOLL_ERR_INVALID_ARG;
+    if (param_dtype == VCOLL_BF16 && (!t.master || !aligned4(t.master))) return VCOLL_ERR_INVALID_ARG;
+    if (state_bits == 8 && (!t.exp_avg_scale || !t.exp_avg_sq_scale || !aligned4(t.exp_avg_scale) ||
+                            !aligned4(t.exp_avg_sq_scale)))
+      return VCOLL_ERR_INVALID_ARG;
+    if (!grid_fits((t.n + kAdamwTile - 1) / kAdamwTile)) return VCOLL_ERR_UNSUPPORTED;
+  }
+  AdamwArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.beta1 = static_cast<float>(hyper->beta1);
+  a.one_minus_beta1 = static_cast<float>(1.0 - hyper->beta1);
+  a.beta2 = static_cast<float>(hyper->beta2);
+  a.one_minus_beta2 = static_cast<float>(1.0 - hyper->beta2);
+  a.grad_scale = static_cast<float>(hyper->grad_scale);
+  a.decay = static_cast<float>(1.0 - hyper->lr * hyper->weight_decay);
+  const double step = static_cast<double>(hyper->step);
+  a.step_size = static_cast<float>(hyper->lr / (1.0 - std::pow(hyper->beta1, step)));
+  a.root_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(hyper->beta2, step)));
+  a.eps = static_cast<float>(hyper->eps);
+  const uint32_t first = mix32(hyper->seed + mix32(static_cast<uint32_t>(hyper->step)));
+  int64_t tiles = 0;
+  const auto run = [&]() {
+    if (a.count == 0) return VCOLL_OK;
+    const vcoll_status st = from_hip(launch_adamw(a, static_cast<int32_t>(tiles), param_dtype, grad_dtype, state_bits,
+                                                  static_cast<hipStream_t>(stream)));
+    a.count = 0;
+    tiles = 0;
+    return st;
+  };
+  for (int k = 0; k < count; ++k) {
+    const vcoll_adamw_tensor& t = tensors[k];
+    if (t.n == 0) continue;
+    const int64_t more = (t.n + kAdamwTile - 1) / kAdamwTile;
+    if (a.count == kAdamwTensors || !grid_fits(tiles + more)) {
+      const vcoll_status st = run();
+      if (st != VCOLL_OK) return st;
+    }
+    AdamwTensor& d = a.t[a.count++];
+    d.n = t.n;
+    d.param = t.param;
+    d.grad = t.grad;
+    d.master = t.master;
+    d.exp_avg = t.exp_avg;
+    d.exp_avg_sq = t.exp_avg_sq;
+    d.exp_avg_scale = t.exp_avg_scale;
+    d.exp_avg_sq_scale = t.exp_avg_sq_scale;
+    d.tile_start = static_cast<int32_t>(tiles);
+    d.key = mix32(first + 0x9E3779B9u * static_cast<uint32_t>(k));
+    tiles += more;
+  }
+  return run();
+}
+
+vcoll_status vcoll_adamw_unpack(int64_t n, const uint8_t* exp_avg, const uint8_t* exp_avg_sq,
+                                const float* exp_avg_scale, const float* exp_avg_sq_scale, float* exp_avg_out,
+                                float* exp_avg_sq_out, void* stream) {
+  if (!valid_count(n)) return VCOLL_ERR_INVALID_ARG;
+  if (!grid_fits((n + kAdamwTile - 1) / kAdamwTile)) return VCOLL_ERR_UNSUPPORTED;
+  if (n == 0) return VCOLL_OK;
+  if (!exp_avg || !exp_avg_sq || !exp_avg_scale || !exp_avg_sq_scale || !exp_avg_out || !exp_avg_sq_out ||
+      !aligned4(exp_avg_scale) || !aligned4(exp_avg_sq_scale) || !aligned4(exp_avg_out) || !aligned4(exp_avg_sq_out))
+    return VCOLL_ERR_INVALID_ARG;
+  UnpackArgs a{exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, exp_avg_out, exp_avg_sq_out, n};
+  return from_hip(launch_unpack(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

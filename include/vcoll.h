@@ -532,6 +532,160 @@ vcoll_status vcoll_model_chain_optimum(int p, double nbytes, double alpha, doubl
 vcoll_status vcoll_model_clock(const vcoll_msg* msgs, int64_t n_msgs, int p, int local, double alpha_in,
                                double beta_in, double alpha_out, double beta_out, double* seconds);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a training step around the collectives: which experts a token
+ * goes to and with what weight, where its rows land, what comes back, and the
+ * update of the parameters once their gradients have been reduced. All run on
+ * the device from device data, so a step needs no copy to the host; each has
+ * its gradient. Float32 arithmetic throughout; a stored bfloat16 element is
+ * rounded once, to nearest even. Results do not depend on the order in which
+ * workgroups run. Rank buffers as above; more than 32 ranks take one launch
+ * per 32.
+ */
+
+/*
+ * MoE router ([NCC] 7.4: every token is sent to its top-k experts). logits[i]
+ * is rank i's [tokens][experts] of dtype (F32 or BF16). For every token, ids
+ * receives the topk experts with the largest logits, largest first, equal
+ * logits (also -0 and +0) by ascending id, and weights their softmax weights
+ * in float32: over the chosen experts with normalise != 0 (a token's weights
+ * then add up to 1), over all of them otherwise. An expert whose logit is
+ * -infinity is never chosen; slots left over hold id -1 and weight 0 (all of
+ * them for a token masked whole). NaN ranks above every number, and a token
+ * with a NaN or +infinity logit has NaN weights. experts <= 1024 and
+ * topk <= 64, else VCOLL_ERR_UNSUPPORTED; topk <= experts.
+ */
+vcoll_status vcoll_moe_route(int p, int64_t tokens, int experts, int topk, vcoll_dtype dtype, int normalise,
+                             const void* const* logits, int32_t* const* ids, float* const* weights, void* stream);
+
+/*
+ * Gradient of vcoll_moe_route's weights: from d_weights (float32
+ * [tokens][topk]) the gradient of the logits, dense, in their dtype,
+ *   d_logits[e] = q[e] ([e = ids[k]] d_weights[k] - sum_j weights[j] d_weights[j]),
+ * q the softmax over the chosen experts (normalise != 0; other experts get
+ * 0, and logits is not read and may be NULL) or over all experts. ids and
+ * weights are the forward call's; a slot whose id is outside [0, experts) is
+ * left out. A token masked whole gets zeros.
+ */
+vcoll_status vcoll_moe_route_backward(int p, int64_t tokens, int experts, int topk, vcoll_dtype dtype, int normalise,
+                                      const void* const* logits, const int32_t* const* ids,
+                                      const float* const* weights, const float* const* d_weights,
+                                      void* const* d_logits, void* stream);
+
+/*
+ * Tokens sorted by expert, on the device ([NCC] 7.4; expert e lives on rank
+ * e / experts_per_rank). ids[i] is rank i's [tokens][topk] (vcoll_moe_route's;
+ * an id outside [0, p*experts_per_rank) means no expert). Rank j's receive
+ * buffer holds the rows of its experts one expert after the other, each
+ * expert's rows ordered by (source rank, token, slot): the stable sort of all
+ * pairs by expert, ready for one product per expert. (The host plan's order,
+ * vcoll_moe_plan, is by source rank first, as blocks arrive from a network.)
+ *   slots[i][t*topk + k] = (j, row) as vcoll_moe_dispatch, vcoll_moe_combine
+ *     and vcoll_moe_combine_weighted take them, (-1, -1) for a pair without
+ *     an expert; 8-byte aligned;
+ *   offsets [p][experts_per_rank + 1] int32: expert j*experts_per_rank + l has
+ *     rows [offsets[j][l], offsets[j][l+1]) of rank j; the last entry is the
+ *     number of rows rank j receives.
+ * workspace: device memory of vcoll_moe_sort_workspace bytes (0 for up to
+ * 1024 pairs; may then be NULL), else VCOLL_ERR_BUFFER_TOO_SMALL. At most 1024
+ * experts in all (VCOLL_ERR_UNSUPPORTED) and 2^31 - 1 pairs. The gradient of
+ * the rows that vcoll_moe_dispatch sends with these slots is
+ * vcoll_moe_combine_weighted with weights NULL.
+ */
+vcoll_status vcoll_moe_sort(int p, int64_t tokens, int topk, int experts_per_rank, const int32_t* const* ids,
+                            int32_t* const* slots, int32_t* offsets, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+vcoll_status vcoll_moe_sort_workspace(int p, int64_t tokens, int topk, int experts_per_rank, int64_t* bytes);
+
+/*
+ * Weighted MoE combine ([NCC] 7.4: each token's result is the weighted sum of
+ * its experts' outputs). For every rank i and token t < tokens
+ *   out[i][t] = sum_k weights[i][t*topk + k] * expert_out[j][r],
+ *   (j, r) = slots[i][t*topk + k],
+ * rows of hidden elements of dtype, summed in float32 in slot order and
+ * rounded once. weights NULL: all ones, which is the gradient of
+ * vcoll_moe_dispatch. A slot outside [0, p) x [0, expert_rows[j]) contributes
+ * nothing (whatever its weight); a token without slots gets zeros. Buffers
+ * must not overlap.
+ */
+vcoll_status vcoll_moe_combine_weighted(int p, int64_t tokens, int topk, int64_t hidden, vcoll_dtype dtype,
+                                        const void* const* expert_out, const int64_t* expert_rows,
+                                        const int32_t* const* slots, const float* const* weights, void* const* out,
+                                        void* stream);
+
+/*
+ * Gradient of vcoll_moe_combine_weighted: from d_out[i] [tokens][hidden]
+ *   d_expert_out[j][r] = weights[i][t*topk + k] * d_out[i][t],
+ *   d_weights[i][t*topk + k] = <d_out[i][t], expert_out[j][r]>  (float32),
+ * (j, r) = slots[i][t*topk + k]. A slot outside the expert buffers gets
+ * d_weights 0; rows of d_expert_out that no slot names are left as they are.
+ * No two slots may name the same row (those of a dispatch never do).
+ */
+vcoll_status vcoll_moe_combine_weighted_backward(int p, int64_t tokens, int topk, int64_t hidden, vcoll_dtype dtype,
+                                                 const void* const* d_out, const void* const* expert_out,
+                                                 const int64_t* expert_rows, const int32_t* const* slots,
+                                                 const float* const* weights, void* const* d_expert_out,
+                                                 float* const* d_weights, void* stream);
+
+/* One tensor of an AdamW step: n elements, every buffer contiguous and
+ * aligned to its element. */
+typedef struct vcoll_adamw_tensor {
+  int64_t n;
+  void* param;              /* F32, or BF16 beside its float32 master copy */
+  const void* grad;         /* F32 or BF16 */
+  float* master;            /* BF16 parameters only (else ignored) */
+  void* exp_avg;            /* float32, or 8-bit codes */
+  void* exp_avg_sq;
+  float* exp_avg_scale;     /* 8-bit states only: one per 128 elements */
+  float* exp_avg_sq_scale;
+} vcoll_adamw_tensor;
+
+typedef struct vcoll_adamw_hyper {
+  double lr, beta1, beta2, eps, weight_decay;
+  double grad_scale;        /* multiplies every gradient, e.g. 1/p after a sum over p ranks */
+  int64_t step;             /* 1, 2, ... */
+  uint32_t seed;            /* of the random rounding of 8-bit states */
+  uint32_t reserved;
+} vcoll_adamw_hyper;
+
+/*
+ * AdamW with decoupled weight decay over `count` tensors at once, in place,
+ * after their gradients were reduced ([HPC] "Communication-Computation
+ * Overlap": the bucket holds many tensors; with a reduce-scatter, the tensors
+ * are this rank's chunks):
+ *   g = grad * grad_scale,  m = beta1 m + (1 - beta1) g,
+ *   v = beta2 v + (1 - beta2) g^2,
+ *   x = (1 - lr weight_decay) x
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps),
+ * float32, every operation rounded to nearest, no fused multiply-add; the
+ * factors are formed in double and rounded to float32 once. x is the F32
+ * parameter or, for BF16, the master copy, whose rounding goes to param.
+ * state_bits 32: m and v are float32. state_bits 8: one byte each and a
+ * float32 scale 2^k per 128 elements of the tensor, k the smallest with
+ * max <= top * 2^k (over the group's finite values, within [-126, 126], 0 for
+ * an all-zero group):
+ *   m: E4M3 (OCP FP8, as vcoll_moe_dispatch_fp8; top 448; NaN and infinities
+ *      store 0x7F);
+ *   v: no sign, 5 exponent bits e and 3 fraction bits f: (8 + f) 2^(e - 34),
+ *      for e = 0 f 2^-33 (top 1.875; NaN and infinities store the top).
+ * Codes are rounded up with a probability that is the fraction lost, in
+ * 1/65536: h = mix(index mod 2^32 + key + mix(index / 2^32)) of the element's
+ * index in its tensor, its high 16 bits for m and its low 16 for v, with
+ * key = mix(mix(seed + mix(step)) + 0x9E3779B9 * tensor) of the tensor's
+ * position in the call and mix(x): x ^= x >> 16, x *= 0x9E3779B1, x ^= x >> 15,
+ * x *= 0x85157AF5, x ^= x >> 16, modulo 2^32. The update uses the m and v of
+ * this step before their rounding. Zeros are a valid initial state. No
+ * buffer may overlap another, and beta1, beta2 are in [0, 1). One launch per
+ * 48 tensors; a captured launch keeps its step.
+ */
+vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dtype param_dtype, vcoll_dtype grad_dtype,
+                         int state_bits, const vcoll_adamw_hyper* hyper, void* stream);
+
+/* The float32 values of n elements of 8-bit AdamW states (0x7F of m is NaN). */
+vcoll_status vcoll_adamw_unpack(int64_t n, const uint8_t* exp_avg, const uint8_t* exp_avg_sq,
+                                const float* exp_avg_scale, const float* exp_avg_sq_scale, float* exp_avg_out,
+                                float* exp_avg_sq_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,220 @@
+"""Training-step operators around the collectives, from their formulas.
+
+Router, expert sort and weighted combine (with gradients) are evaluated in
+float64 on the exact values of their inputs, so that a test can bound the
+library's float32 rounding against them. The AdamW step is float32 by
+definition (each operation rounded once, no fused multiply-add), so numpy
+float32 arrays give its exact bits; its 8-bit codes are built from values,
+not from bit patterns.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+GROUP = 128
+
+
+# --- router ------------------------------------------------------------------
+
+def route(z: np.ndarray, topk: int, normalise: bool):
+    """z [T, E] float64 -> (ids [T, topk] int32, weights [T, topk])."""
+    T, E = z.shape
+    ids = np.full((T, topk), -1, np.int32)
+    w = np.zeros((T, topk))
+    for t in range(T):
+        row = z[t]
+        # NaN first, then descending; equal values by ascending id
+        order = sorted(range(E), key=lambda e: (0, 0.0, e) if np.isnan(row[e]) else (1, -row[e], e))
+        live = [e for e in order[:topk] if not row[e] == -np.inf]
+        if not live:
+            continue
+        ids[t, :len(live)] = live
+        if np.isnan(row).any() or np.isposinf(row).any():
+            w[t, :len(live)] = np.nan
+            continue
+        among = row[live] if normalise else row
+        w[t, :len(live)] = np.exp(row[live] - row[live[0]]) / np.exp(among - row[live[0]]).sum()
+    return ids, w
+
+
+def route_backward(z: np.ndarray, ids: np.ndarray, d_weights: np.ndarray, normalise: bool) -> np.ndarray:
+    """Gradient of route's weights with respect to z [T, E], by the Jacobian of the softmax."""
+    T, E = z.shape
+    dz = np.zeros((T, E))
+    for t in range(T):
+        live = [(k, int(e)) for k, e in enumerate(ids[t]) if 0 <= e < E]
+        among = [e for _, e in live] if normalise else [e for e in range(E) if z[t, e] > -np.inf]
+        if not among:
+            continue
+        q = np.exp(z[t, among] - z[t, among].max())
+        q /= q.sum()
+        jac = np.diag(q) - np.outer(q, q)                 # d q_a / d z_b
+        up = np.zeros(len(among))
+        for k, e in live:
+            if e in among:
+                up[among.index(e)] += d_weights[t, k]
+        dz[t, among] = jac @ up
+    return dz
+
+
+# --- expert sort ---------------------------------------------------------------
+
+def expert_sort(ids: np.ndarray, experts_per_rank: int):
+    """ids [p, T, K] -> (slots [p, T*K, 2], offsets [p, experts_per_rank + 1])."""
+    p, T, K = ids.shape
+    rows = [[] for _ in range(p * experts_per_rank)]      # (source rank, pair) in order
+    for i in range(p):
+        for x, e in enumerate(ids[i].reshape(-1)):
+            if 0 <= e < p * experts_per_rank:
+                rows[e].append((i, x))
+    slots = np.full((p, T * K, 2), -1, np.int32)
+    offsets = np.zeros((p, experts_per_rank + 1), np.int32)
+    for j in range(p):
+        at = 0
+        for l in range(experts_per_rank):
+            for i, x in rows[j * experts_per_rank + l]:
+                slots[i, x] = (j, at)
+                at += 1
+            offsets[j, l + 1] = at
+    return slots, offsets
+
+
+# --- weighted combine ----------------------------------------------------------
+
+def _valid(slot, expert_out) -> bool:
+    j, r = int(slot[0]), int(slot[1])
+    return 0 <= j < len(expert_out) and 0 <= r < expert_out[j].shape[0]
+
+
+def combine_weighted(expert_out: list, slots: np.ndarray, weights, tokens: int, topk: int):
+    """(out [p, tokens, H], sum_k |w e| of the same shape) in float64."""
+    p, H = len(slots), expert_out[0].shape[1]
+    out, size = np.zeros((p, tokens, H)), np.zeros((p, tokens, H))
+    for i in range(p):
+        for t in range(tokens):
+            for k in range(topk):
+                s = slots[i][t * topk + k]
+                if _valid(s, expert_out):
+                    w = 1.0 if weights is None else weights[i][t, k]
+                    term = w * expert_out[s[0]][s[1]].astype(np.float64)
+                    out[i, t] += term
+                    size[i, t] += np.abs(term)
+    return out, size
+
+
+def combine_weighted_backward(d_out: np.ndarray, expert_out: list, slots: np.ndarray, weights: np.ndarray, topk: int):
+    """(d_expert_out: p arrays, NaN where no slot names the row; d_weights;
+    sum |dy e| of d_weights' shape) in float64."""
+    p, T, _ = d_out.shape
+    d_expert = [np.full(e.shape, np.nan) for e in expert_out]
+    dw, size = np.zeros((p, T, topk)), np.zeros((p, T, topk))
+    for i in range(p):
+        for t in range(T):
+            for k in range(topk):
+                s = slots[i][t * topk + k]
+                if _valid(s, expert_out):
+                    e = expert_out[s[0]][s[1]].astype(np.float64)
+                    d_expert[s[0]][s[1]] = float(weights[i][t, k]) * d_out[i, t]
+                    dw[i, t, k] = (d_out[i, t] * e).sum()
+                    size[i, t, k] = np.abs(d_out[i, t] * e).sum()
+    return d_expert, dw, size
+
+
+# --- AdamW ----------------------------------------------------------------------
+
+def mix(x: np.ndarray) -> np.ndarray:
+    x = np.asarray(x, dtype=np.uint64) & np.uint64(0xFFFFFFFF)
+    mask = np.uint64(0xFFFFFFFF)
+    x = x ^ (x >> np.uint64(16))
+    x = (x * np.uint64(0x9E3779B1)) & mask
+    x = x ^ (x >> np.uint64(15))
+    x = (x * np.uint64(0x85157AF5)) & mask
+    return x ^ (x >> np.uint64(16))
+
+
+def rounding_bits(n: int, seed: int, step: int, tensor: int) -> np.ndarray:
+    """The 32 random bits of elements 0..n-1 of the call's tensor number `tensor`."""
+    first = mix(seed + int(mix(step)))
+    key = mix(int(first) + 0x9E3779B9 * tensor & 0xFFFFFFFF)
+    return mix(np.arange(n, dtype=np.uint64) + np.uint64(key))
+
+
+class Format:
+    """An 8-bit float: 3 fraction bits, smallest normal 2^low, largest value `top`."""
+
+    def __init__(self, low: int, top: float):
+        self.low, self.top = low, top
+
+    def value(self, code: np.ndarray) -> np.ndarray:
+        code = np.asarray(code, dtype=np.int64)
+        e, f = code >> 3, code & 7
+        return np.where(e == 0, f * 2.0 ** (self.low - 3), (8 + f) * np.exp2(e.astype(np.float64) - 1 + self.low - 3))
+
+    def round(self, y: np.ndarray, up: np.ndarray) -> np.ndarray:
+        """Codes of y >= 0: the code below, plus one where the lost fraction in
+        2^-20 of a step, plus the random `up` in 2^-20, reaches a whole step."""
+        y = y.astype(np.float64)
+        _, e = np.frexp(y)
+        step_exp = np.maximum(e - 1, self.low) - 3
+        units = np.floor(y * np.exp2(20.0 - step_exp)).astype(np.int64)      # exact: y has 24 bits
+        steps = (units + up.astype(np.int64)) >> 20
+        # steps counts fractions of a binade: 8..15 in a normal one (16: the next one's first)
+        return np.where(y == 0, up.astype(np.int64) >> 20, steps + 8 * (step_exp + 3 - self.low))
+
+
+M_FORMAT = Format(-6, 448.0)
+V_FORMAT = Format(-30, 1.875)
+
+
+def _scales(x: np.ndarray, top: float) -> np.ndarray:
+    """Per group of 128 the smallest power of two s with max|finite x| <= top * s."""
+    n = x.size
+    out = np.ones(-(-n // GROUP), np.float32)
+    for b in range(out.size):
+        a = np.abs(x[b * GROUP:(b + 1) * GROUP].astype(np.float64))
+        a = a[np.isfinite(a)]
+        amax = a.max() if a.size else 0.0
+        if amax > 0:
+            k = -126
+            while amax > top * 2.0 ** k and k < 126:
+                k += 1
+            out[b] = 2.0 ** k
+    return out
+
+
+def encode_m(m: np.ndarray, bits: np.ndarray):
+    s = _scales(m, M_FORMAT.top)
+    y = m / np.repeat(s, GROUP)[:m.size]
+    fine = np.isfinite(y)
+    code = M_FORMAT.round(np.where(fine, np.abs(y), 0), (bits >> np.uint64(16)) << np.uint64(4)) | np.where(y < 0, 128, 0)
+    return np.where(fine, code, 0x7F).astype(np.uint8), s
+
+
+def encode_v(v: np.ndarray, bits: np.ndarray):
+    s = _scales(v, V_FORMAT.top)
+    y = v / np.repeat(s, GROUP)[:v.size]
+    fine = np.isfinite(y) & (y <= V_FORMAT.top)
+    code = V_FORMAT.round(np.where(fine, y, 0), (bits & np.uint64(0xFFFF)) << np.uint64(4))
+    return np.where(fine, code, 0xFF).astype(np.uint8), s
+
+
+def decode_m(code: np.ndarray, s: np.ndarray) -> np.ndarray:
+    a = M_FORMAT.value(code & 0x7F).astype(np.float32)
+    a = np.where((code & 0x7F) == 0x7F, np.float32(np.nan), a)
+    return np.where(code & 0x80, -a, a) * np.repeat(s, GROUP)[:code.size]
+
+
+def decode_v(code: np.ndarray, s: np.ndarray) -> np.ndarray:
+    return V_FORMAT.value(code).astype(np.float32) * np.repeat(s, GROUP)[:code.size]
+
+
+def adamw(x: np.ndarray, grad: np.ndarray, m: np.ndarray, v: np.ndarray, *, lr, beta1, beta2, eps, weight_decay, step,
+          grad_scale):
+    """One float32 step: (x, m, v)."""
+    f = np.float32
+    g = grad.astype(f) * f(grad_scale)
+    m = m * f(beta1) + g * f(1.0 - beta1)
+    v = v * f(beta2) + (g * g) * f(1.0 - beta2)
+    move = m / (np.sqrt(v) * f(1.0 / np.sqrt(1.0 - beta2 ** step)) + f(eps))
+    x = x * f(1.0 - lr * weight_decay) - move * f(lr / (1.0 - beta1 ** step))
+    return x, m, v
