@@ -61,7 +61,7 @@ struct WeightedArgs {
   void* out[kTokenRanks];              // [tokens][hidden]
   int64_t tokens, hidden;
   int32_t topk, p;
-  int32_t vec;                         // rows and bases 16-byte aligned
+  int32_t segments;                    // workgroups per token, each one segment of the row (set by the launcher)
   int32_t ranks;
 };
 static_assert(sizeof(WeightedArgs) <= 4096, "kernel arguments are limited to 4 KiB");
@@ -76,8 +76,8 @@ struct WeightedBackwardArgs {
   float* d_weights[kTokenRanks];       // [tokens * topk]
   int64_t tokens, hidden;
   int32_t topk, p;
-  int32_t vec;
   int32_t ranks;
+  int32_t pad;
 };
 static_assert(sizeof(WeightedBackwardArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 

@@ -62,15 +62,19 @@ int64_t sort_bytes(int64_t pairs, int64_t experts) {
   return blocks > 1 ? blocks * experts * 4 : 0;
 }
 
+constexpr int64_t kMaxHidden = int64_t(1) << 28;   // rows of up to 1 GiB: byte offsets in a row are int32
+
 vcoll_status check_rows(int p, int64_t tokens, int topk, int64_t hidden, int dtype, const int64_t* expert_rows) {
   if (!valid_p(p) || !valid_count(tokens) || topk < 1 || !valid_count(hidden) || !valid_dtype(dtype) || !expert_rows)
     return VCOLL_ERR_INVALID_ARG;
-  if (!pairs_fit(tokens, topk) || hidden > INT32_MAX / 4) return VCOLL_ERR_INVALID_ARG;
+  if (!pairs_fit(tokens, topk) || hidden > kMaxHidden) return VCOLL_ERR_INVALID_ARG;
   const int64_t rb = hidden * elem_bytes(static_cast<vcoll_dtype>(dtype));
   if (!fits(tokens, rb)) return VCOLL_ERR_INVALID_ARG;
   for (int j = 0; j < p; ++j)
     if (expert_rows[j] < 0 || expert_rows[j] > INT32_MAX || !fits(expert_rows[j], rb)) return VCOLL_ERR_INVALID_ARG;
-  return grid_fits(tokens) ? VCOLL_OK : VCOLL_ERR_UNSUPPORTED;
+  // one workgroup of up to 1024 threads per token, or of 64 threads per KiB of its row
+  const bool fit = grid_fits(tokens) && tokens * std::max<int64_t>(1, (rb + 1023) / 1024) <= (int64_t(UINT32_MAX) >> 6);
+  return fit ? VCOLL_OK : VCOLL_ERR_UNSUPPORTED;
 }
 
 bool valid_hyper(const vcoll_adamw_hyper* h) {
@@ -190,12 +194,10 @@ vcoll_status vcoll_moe_combine_weighted(int p, int64_t tokens, int topk, int64_t
   if (tokens == 0 || hidden == 0) return VCOLL_OK;
   if (!expert_out || !all_given(p, slots) || !all_set(p, out) || (weights && !all_given(p, weights)))
     return VCOLL_ERR_INVALID_ARG;
-  bool vec = hidden * elem_bytes(dtype) % 16 == 0;
   for (int j = 0; j < p; ++j) {
     if (expert_rows[j] > 0 && (!expert_out[j] || !aligned_to(expert_out[j], dtype))) return VCOLL_ERR_INVALID_ARG;
     if (!aligned_to(out[j], dtype) || !aligned4(slots[j]) || (weights && !aligned4(weights[j])))
       return VCOLL_ERR_INVALID_ARG;
-    vec = vec && aligned16(out[j]) && (expert_rows[j] == 0 || aligned16(expert_out[j]));
   }
   return by_ranks(p, [&](int i0, int n) {
     WeightedArgs a;
@@ -213,7 +215,6 @@ vcoll_status vcoll_moe_combine_weighted(int p, int64_t tokens, int topk, int64_t
     a.hidden = hidden;
     a.topk = topk;
     a.p = p;
-    a.vec = vec;
     a.ranks = n;
     return from_hip(launch_weighted(a, dtype, static_cast<hipStream_t>(stream)));
   });
@@ -231,7 +232,6 @@ vcoll_status vcoll_moe_combine_weighted_backward(int p, int64_t tokens, int topk
   if (!expert_out || !d_expert_out || !all_given(p, slots) || !all_given(p, weights) || !all_given(p, d_weights) ||
       !all_set(p, d_out))
     return VCOLL_ERR_INVALID_ARG;
-  bool vec = hidden * elem_bytes(dtype) % 16 == 0;
   for (int j = 0; j < p; ++j) {
     const bool rows = expert_rows[j] > 0;
     if (rows && (!expert_out[j] || !d_expert_out[j] || !aligned_to(expert_out[j], dtype) ||
@@ -239,7 +239,6 @@ vcoll_status vcoll_moe_combine_weighted_backward(int p, int64_t tokens, int topk
       return VCOLL_ERR_INVALID_ARG;
     if (!aligned_to(d_out[j], dtype) || !aligned4(slots[j]) || !aligned4(weights[j]) || !aligned4(d_weights[j]))
       return VCOLL_ERR_INVALID_ARG;
-    vec = vec && aligned16(d_out[j]) && (!rows || (aligned16(expert_out[j]) && aligned16(d_expert_out[j])));
   }
   return by_ranks(p, [&](int i0, int n) {
     WeightedBackwardArgs a;
@@ -259,7 +258,6 @@ vcoll_status vcoll_moe_combine_weighted_backward(int p, int64_t tokens, int topk
     a.hidden = hidden;
     a.topk = topk;
     a.p = p;
-    a.vec = vec;
     a.ranks = n;
     return from_hip(launch_weighted_backward(a, dtype, static_cast<hipStream_t>(stream)));
   });

@@ -4,10 +4,18 @@
 //   d_expert[slot]  = w[t, k] * d_out[t]
 //   d_weights[t, k] = <d_out[t], expert_out[slot(t, k)]>
 //
-// One workgroup per token: the token's row stays in registers while the rows
-// of its slots stream past, so every byte moves once. Sums are float32, over
-// k in slot order; one rounding per stored element. A slot outside the expert
-// buffers contributes nothing.
+// Every byte moves once: a lane loads its vector of all the token's expert
+// rows before it uses the first. Sums are float32 (fused multiply-adds over
+// k in slot order); one rounding per stored element. A slot outside the
+// expert buffers contributes nothing.
+//
+// The rows of up to 64 slots are looked up at once, one per lane, and each
+// then becomes a wave-uniform buffer resource. Looking them up one after the
+// other would put 2 K dependent scalar loads before the first row load. A
+// slot without a row gets a resource of no bytes: its loads return zeros and
+// its stores are dropped, so the loops over rows need no branches.
+#include <algorithm>
+
 #include "device.h"
 #include "train.h"
 
@@ -16,145 +24,252 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRowsInFlight = 8;   // slots whose loads are issued together
+// Expert rows are read once and written once, so both stream past the caches.
+// On MI355X, with the rows of 8 x 4096 tokens x 8 experts x 7168 bf16 (3.76
+// GB) read and the 0.47 GB of outputs written, the combine takes 716 us (5.9
+// TB/s; a copy runs at 6.4, reads alone at 7.0), 760 us with cached loads and
+// 765 us with cached stores; its gradient, which also writes 3.76 GB, takes
+// 1511 us (5.3 TB/s), 1557 us with cached stores, and does not respond to the
+// rows in flight (8: 1513, 4: 1529, 2: 1531), to pauses between its stores,
+// or to the distance between the two expert buffers: the mix of row-sized
+// reads and writes all over memory bounds it.
+constexpr int kRowPolicy = kPolicyNT;
 
-template <int D>
-__global__ __launch_bounds__(kBlock) void weighted_kernel(const WeightedArgs a) {
+// Combine: one-wave workgroups, each one 1 KiB segment of the token's row (two
+// vectors per lane 740 us, four-wave workgroups 765, seven-wave 727).
+constexpr int kSegment = 64 * 16;
+
+// Gradient: a workgroup holds whole rows, because a dot product ends in one
+// number: one 16-byte vector per lane in up to 16 waves, longer rows in
+// several steps (two vectors per lane in half as many waves: 1540 us).
+constexpr int kTokenWaves = 16;
+
+// One lane's slot: the address of its row (0: none) and its weight.
+struct Row {
+  uint64_t at;
+  uint64_t d_at;
+  float weight;
+};
+
+__device__ __forceinline__ uint64_t lane_u64(uint64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(x), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(x >> 32), lane);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+
+__device__ __forceinline__ float lane_float(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
+}
+
+// The first `bytes` bytes from a wave-uniform address; none from address 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(uint64_t at, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, at ? bytes : 0, kRawBufferFormat);
+}
+
+template <class Args>
+__device__ __forceinline__ int64_t row_of(const Args& a, const int32_t* slot, int k, int& j) {
+  j = slot[2 * k];
+  const int r = slot[2 * k + 1];
+  if (j < 0 || j >= a.p || r < 0 || r >= a.expert_rows[j]) return -1;
+  return r;
+}
+
+template <int D, int Q>
+__global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
   using S = Storage<D>;
   using E = typename S::elem;
   constexpr int VE = S::kVE;
-  const int tid = threadIdx.x;
+  const int lane = threadIdx.x;
   const int i = blockIdx.y;
-  const int64_t t = blockIdx.x;
+  const int seg = static_cast<int>(blockIdx.x % a.segments);
+  const int64_t t = blockIdx.x / a.segments;
   const int32_t* slot = a.slots[i] + 2 * t * a.topk;
-  const float* weight = a.weights[i] ? a.weights[i] + t * a.topk : nullptr;
+  const int row_bytes = static_cast<int>(a.hidden * sizeof(E));
+  const int whole = row_bytes / 16 * 16;
   E* out = static_cast<E*>(a.out[i]) + t * a.hidden;
-  auto source = [&](int k) -> const E* {
-    const int j = slot[2 * k], r = slot[2 * k + 1];
-    if (j < 0 || j >= a.p || r < 0 || r >= a.expert_rows[j]) return nullptr;
-    return static_cast<const E*>(a.expert_out[j]) + r * a.hidden;
-  };
-  const int64_t nvec = a.vec ? a.hidden / VE : 0;
-  for (int64_t x = tid; x < nvec; x += kBlock) {
-    float sum[VE] = {};
-    for (int k0 = 0; k0 < a.topk; k0 += kRowsInFlight) {
-      u32x4 row[kRowsInFlight];
-      float w[kRowsInFlight];
-#pragma unroll
-      for (int q = 0; q < kRowsInFlight; ++q) {
-        const E* src = k0 + q < a.topk ? source(k0 + q) : nullptr;
-        w[q] = src && weight ? weight[k0 + q] : 1.0f;
-        row[q] = src ? ld16(src, x * 16) : u32x4{0, 0, 0, 0};
-        if (!src) w[q] = 0.0f;
+  const auto out_rsrc = row_rsrc(reinterpret_cast<uint64_t>(out), whole);
+  float sum[VE] = {};
+  float tail = 0.0f;                                 // element whole / sizeof(E) + lane of the row
+  const int off = seg * kSegment + lane * 16;
+  const int tail_off = whole + lane * static_cast<int>(sizeof(E));
+  const bool has_tail = seg == 0 && tail_off < row_bytes;
+  for (int k0 = 0; k0 < a.topk; k0 += 64) {
+    Row mine = {0, 0, 0.0f};
+    if (k0 + lane < a.topk) {
+      int j;
+      const int64_t r = row_of(a, slot, k0 + lane, j);
+      if (r >= 0) {
+        mine.at = reinterpret_cast<uint64_t>(static_cast<const E*>(a.expert_out[j]) + r * a.hidden);
+        mine.weight = a.weights[i] ? a.weights[i][t * a.topk + k0 + lane] : 1.0f;
       }
+    }
+    const int kn = a.topk - k0 < 64 ? a.topk - k0 : 64;
+    for (int k1 = 0; k1 < kn; k1 += Q) {
+      u32x4 row[Q];
 #pragma unroll
-      for (int q = 0; q < kRowsInFlight; ++q) {
+      for (int q = 0; q < Q; ++q)
+        row[q] = __builtin_amdgcn_raw_buffer_load_b128(row_rsrc(lane_u64(mine.at, k1 + q), whole), off, 0, kRowPolicy);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const float w = lane_float(mine.weight, k1 + q);
         float f[VE];
         S::widen(row[q], f);
 #pragma unroll
-        for (int c = 0; c < VE; ++c) sum[c] += w[q] * f[c];
+        for (int c = 0; c < VE; ++c) sum[c] = __builtin_fmaf(w, f[c], sum[c]);
       }
     }
-    st16(out, x * 16, S::narrow(sum));
-  }
-  for (int64_t x = nvec * VE + tid; x < a.hidden; x += kBlock) {
-    float sum = 0.0f;
-    for (int k = 0; k < a.topk; ++k) {
-      const E* src = source(k);
-      if (src) sum += (weight ? weight[k] : 1.0f) * S::widen1(src[x]);
+    if (whole != row_bytes) {
+      for (int k = 0; k < kn; ++k) {
+        const char* src = reinterpret_cast<const char*>(lane_u64(mine.at, k));
+        const float w = lane_float(mine.weight, k);
+        if (src && has_tail)
+          tail = __builtin_fmaf(w, S::widen1(*reinterpret_cast<const E*>(src + tail_off)), tail);
+      }
     }
-    out[x] = S::narrow1(sum);
+  }
+  __builtin_amdgcn_raw_buffer_store_b128(S::narrow(sum), out_rsrc, off, 0, kRowPolicy);
+  if (has_tail) *reinterpret_cast<E*>(reinterpret_cast<char*>(out) + tail_off) = S::narrow1(tail);
+}
+
+// Sum of each of Q (a power of two) values over the 64 lanes of a wave, value
+// q left in the lanes with lane % Q == q: halving the number of values while
+// lanes pair up takes Q - 1 + log2(64 / Q) shuffles.
+template <int Q>
+__device__ __forceinline__ float wave_sums(const float* x, int lane) {
+  if constexpr (Q == 1) {
+    return x[0];
+  } else {
+    float y[Q / 2];
+    const bool high = (lane & (Q / 2)) != 0;
+#pragma unroll
+    for (int q = 0; q < Q / 2; ++q) {
+      const float keep = high ? x[q + Q / 2] : x[q], give = high ? x[q] : x[q + Q / 2];
+      y[q] = keep + __shfl_xor(give, Q / 2);
+    }
+    return wave_sums<Q / 2>(y, lane);
   }
 }
 
-template <int D>
-__global__ __launch_bounds__(kBlock) void weighted_backward_kernel(const WeightedBackwardArgs a) {
+template <int D, int Q>
+__global__ __launch_bounds__(kTokenWaves * 64) void weighted_backward_kernel(const WeightedBackwardArgs a) {
   using S = Storage<D>;
   using E = typename S::elem;
   constexpr int VE = S::kVE;
-  __shared__ float part[kBlock / 64][kRowsInFlight];
+  __shared__ float part[kTokenWaves][Q];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  const int threads = blockDim.x, waves = threads / 64;
   const int i = blockIdx.y;
   const int64_t t = blockIdx.x;
   const int32_t* slot = a.slots[i] + 2 * t * a.topk;
-  const float* weight = a.weights[i] + t * a.topk;
   const E* dy = static_cast<const E*>(a.d_out[i]) + t * a.hidden;
-  const int64_t nvec = a.vec ? a.hidden / VE : 0;
-  for (int k0 = 0; k0 < a.topk; k0 += kRowsInFlight) {
-    const E* src[kRowsInFlight];
-    E* dst[kRowsInFlight];
-    float w[kRowsInFlight], dot[kRowsInFlight];
-#pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q) {
-      src[q] = nullptr;
-      dst[q] = nullptr;
-      w[q] = dot[q] = 0.0f;
-      if (k0 + q < a.topk) {
-        const int j = slot[2 * (k0 + q)], r = slot[2 * (k0 + q) + 1];
-        if (j >= 0 && j < a.p && r >= 0 && r < a.expert_rows[j]) {
-          src[q] = static_cast<const E*>(a.expert_out[j]) + r * a.hidden;
-          dst[q] = static_cast<E*>(a.d_expert_out[j]) + r * a.hidden;
-          w[q] = weight[k0 + q];
-        }
+  const int row_bytes = static_cast<int>(a.hidden * sizeof(E));
+  const int whole = row_bytes / 16 * 16;
+  const auto dy_rsrc = row_rsrc(reinterpret_cast<uint64_t>(dy), whole);
+  const int tail_off = whole + tid * static_cast<int>(sizeof(E));
+  for (int k0 = 0; k0 < a.topk; k0 += 64) {
+    Row mine = {0, 0, 0.0f};
+    if (k0 + lane < a.topk) {
+      int j;
+      const int64_t r = row_of(a, slot, k0 + lane, j);
+      if (r >= 0) {
+        mine.at = reinterpret_cast<uint64_t>(static_cast<const E*>(a.expert_out[j]) + r * a.hidden);
+        mine.d_at = reinterpret_cast<uint64_t>(static_cast<E*>(a.d_expert_out[j]) + r * a.hidden);
+        mine.weight = a.weights[i][t * a.topk + k0 + lane];
       }
     }
-    for (int64_t x = tid; x < nvec; x += kBlock) {
-      u32x4 row[kRowsInFlight];
+    const int kn = a.topk - k0 < 64 ? a.topk - k0 : 64;
+    for (int k1 = 0; k1 < kn; k1 += Q) {
+      float dot[Q] = {};
+      for (int off = tid * 16; off - tid * 16 < whole; off += threads * 16) {
+        const u32x4 g4 = __builtin_amdgcn_raw_buffer_load_b128(dy_rsrc, off, 0, kPolicyCached);
+        u32x4 row[Q];
 #pragma unroll
-      for (int q = 0; q < kRowsInFlight; ++q) row[q] = src[q] ? ld16(src[q], x * 16) : u32x4{0, 0, 0, 0};
-      float g[VE];
-      S::widen(*reinterpret_cast<const u32x4*>(dy + x * VE), g);
+        for (int q = 0; q < Q; ++q)
+          row[q] = __builtin_amdgcn_raw_buffer_load_b128(row_rsrc(lane_u64(mine.at, k1 + q), whole), off, 0, kRowPolicy);
+        float g[VE];
+        S::widen(g4, g);
 #pragma unroll
-      for (int q = 0; q < kRowsInFlight; ++q) {
-        if (!src[q]) continue;
-        float f[VE], d[VE];
-        S::widen(row[q], f);
+        for (int q = 0; q < Q; ++q) {
+          const float w = lane_float(mine.weight, k1 + q);
+          float f[VE], d[VE];
+          S::widen(row[q], f);
 #pragma unroll
-        for (int c = 0; c < VE; ++c) {
-          dot[q] += g[c] * f[c];
-          d[c] = w[q] * g[c];
+          for (int c = 0; c < VE; ++c) {
+            dot[q] = __builtin_fmaf(g[c], f[c], dot[q]);
+            d[c] = w * g[c];
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(S::narrow(d), row_rsrc(lane_u64(mine.d_at, k1 + q), whole), off, 0,
+                                                 kRowPolicy);
         }
-        st16(dst[q], x * 16, S::narrow(d));
       }
-    }
-    for (int64_t x = nvec * VE + tid; x < a.hidden; x += kBlock) {
-      const float g = S::widen1(dy[x]);
+      if (whole != row_bytes) {
+        const bool has_tail = tail_off < row_bytes;
+        const float g = has_tail ? S::widen1(*reinterpret_cast<const E*>(reinterpret_cast<const char*>(dy) + tail_off)) : 0.0f;
 #pragma unroll
-      for (int q = 0; q < kRowsInFlight; ++q)
-        if (src[q]) {
-          dot[q] += g * S::widen1(src[q][x]);
-          dst[q][x] = S::narrow1(w[q] * g);
+        for (int q = 0; q < Q; ++q) {
+          const uint64_t at = lane_u64(mine.at, k1 + q), d_at = lane_u64(mine.d_at, k1 + q);
+          const float w = lane_float(mine.weight, k1 + q);
+          if (at && has_tail) {
+            dot[q] = __builtin_fmaf(g, S::widen1(*reinterpret_cast<const E*>(at + tail_off)), dot[q]);
+            *reinterpret_cast<E*>(d_at + tail_off) = S::narrow1(w * g);
+          }
         }
-    }
+      }
+      float sum = wave_sums<Q>(dot, lane);
 #pragma unroll
-    for (int q = 0; q < kRowsInFlight; ++q) {
-#pragma unroll
-      for (int m = 32; m > 0; m >>= 1) dot[q] += __shfl_xor(dot[q], m);
-      if (lane == 0) part[wave][q] = dot[q];
+      for (int m = Q; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+      if (lane < Q) part[wave][lane] = sum;
+      __syncthreads();
+      if (tid < Q && k1 + tid < kn) {
+        sum = 0.0f;
+        for (int v = 0; v < waves; ++v) sum += part[v][tid];
+        a.d_weights[i][t * a.topk + k0 + k1 + tid] = sum;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (tid < kRowsInFlight && k0 + tid < a.topk) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int v = 0; v < kBlock / 64; ++v) sum += part[v][tid];
-      a.d_weights[i][t * a.topk + k0 + tid] = sum;
-    }
-    __syncthreads();
   }
+}
+
+template <int D, int Q>
+hipError_t launch_weighted_q(WeightedArgs a, hipStream_t stream) {
+  const int64_t row_bytes = a.hidden * sizeof(typename Storage<D>::elem);
+  a.segments = static_cast<int32_t>(row_bytes > kSegment ? (row_bytes / 16 * 16 + kSegment - 1) / kSegment : 1);
+  const dim3 grid(static_cast<unsigned>(a.tokens * a.segments), a.ranks);
+  return launch(weighted_kernel<D, Q>, grid, 64, a, stream);
+}
+
+template <int D, int Q>
+hipError_t launch_weighted_backward_q(const WeightedBackwardArgs& a, hipStream_t stream) {
+  const int64_t vecs = a.hidden * sizeof(typename Storage<D>::elem) / 16;
+  const int block = 64 * static_cast<int>(std::min<int64_t>(kTokenWaves, std::max<int64_t>(1, (vecs + 63) / 64)));
+  const dim3 grid(static_cast<unsigned>(a.tokens), a.ranks);
+  return launch(weighted_backward_kernel<D, Q>, grid, block, a, stream);
+}
+
+// Q: rows in flight, the chosen experts of a token where they are few.
+template <int D>
+hipError_t launch_weighted_dt(const WeightedArgs& a, hipStream_t stream) {
+  if (a.topk <= 2) return launch_weighted_q<D, 2>(a, stream);
+  if (a.topk <= 4) return launch_weighted_q<D, 4>(a, stream);
+  return launch_weighted_q<D, 8>(a, stream);
+}
+
+template <int D>
+hipError_t launch_weighted_backward_dt(const WeightedBackwardArgs& a, hipStream_t stream) {
+  if (a.topk <= 2) return launch_weighted_backward_q<D, 2>(a, stream);
+  if (a.topk <= 4) return launch_weighted_backward_q<D, 4>(a, stream);
+  return launch_weighted_backward_q<D, 8>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_weighted(const WeightedArgs& a, vcoll_dtype dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.tokens), a.ranks);
-  if (dtype == VCOLL_F32) return launch(weighted_kernel<VCOLL_F32>, grid, a, stream);
-  return launch(weighted_kernel<VCOLL_BF16>, grid, a, stream);
+  return dtype == VCOLL_F32 ? launch_weighted_dt<VCOLL_F32>(a, stream) : launch_weighted_dt<VCOLL_BF16>(a, stream);
 }
 
 hipError_t launch_weighted_backward(const WeightedBackwardArgs& a, vcoll_dtype dtype, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.tokens), a.ranks);
-  if (dtype == VCOLL_F32) return launch(weighted_backward_kernel<VCOLL_F32>, grid, a, stream);
-  return launch(weighted_backward_kernel<VCOLL_BF16>, grid, a, stream);
+  return dtype == VCOLL_F32 ? launch_weighted_backward_dt<VCOLL_F32>(a, stream)
+                            : launch_weighted_backward_dt<VCOLL_BF16>(a, stream);
 }
 
 }  // namespace vcoll

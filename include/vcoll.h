@@ -606,7 +606,7 @@ vcoll_status vcoll_moe_sort_workspace(int p, int64_t tokens, int topk, int exper
  * rounded once. weights NULL: all ones, which is the gradient of
  * vcoll_moe_dispatch. A slot outside [0, p) x [0, expert_rows[j]) contributes
  * nothing (whatever its weight); a token without slots gets zeros. Buffers
- * must not overlap.
+ * must not overlap and need only be aligned to their elements. hidden <= 2^28.
  */
 vcoll_status vcoll_moe_combine_weighted(int p, int64_t tokens, int topk, int64_t hidden, vcoll_dtype dtype,
                                         const void* const* expert_out, const int64_t* expert_rows,
