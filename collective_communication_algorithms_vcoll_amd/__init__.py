@@ -282,6 +282,20 @@ def _disjoint(ts: list, what: str) -> None:
             raise ValueError(f"{what}: output buffers overlap")
 
 
+def _apart(ins, outs, what: str) -> None:
+    """_no_overlap(ins, outs) and _disjoint(outs) in one sweep over the spans."""
+    spans = [(t.data_ptr(), 0, t.nbytes) for t in ins]
+    spans += [(t.data_ptr(), 1, t.nbytes) for t in outs]
+    spans.sort()
+    end = [0, 0]                                  # where the inputs and the outputs seen so far end
+    for s0, side, size in spans:
+        if size and (s0 < end[1] or (side and s0 < end[0])):
+            raise ValueError(f"{what}: " + ("output buffers overlap" if side and s0 < end[1]
+                                            else "input and output buffers overlap"))
+        if size and s0 + size > end[side]:
+            end[side] = s0 + size
+
+
 # -----------------------------------------------------------------------------
 
 
@@ -756,17 +770,19 @@ def vcoll_moe_dispatch(tokens, slots, recv_rows, topk: int, fp8: bool = False, r
     r = list(recv)
     orb = H + H // 32 if fp8 else H * t[0].element_size()
     for j in range(p):
-        if not r[j].is_contiguous() or r[j].numel() * r[j].element_size() < rr[j] * orb:
+        if not r[j].is_contiguous() or r[j].nbytes < rr[j] * orb:
             raise ValueError(f"vcoll_moe_dispatch: recv[{j}] holds fewer than {rr[j]} rows")
+        if r[j].device != dev:
+            raise ValueError(f"vcoll_moe_dispatch: recv[{j}] is on {r[j].device}, the token tables on {dev}")
     s = list(slots)
     for x in s:
         if x.dtype != torch.int32 or x.device != dev or x.numel() < 2 * T * topk:
             raise ValueError("vcoll_moe_dispatch: slots must be int32 GPU tensors of T*topk pairs")
-    _no_overlap(t, r, "vcoll_moe_dispatch")
-    _disjoint(r, "vcoll_moe_dispatch")
-    rows = (ctypes.c_int64 * p)(*rr)
-    _check(_lib().vcoll_moe_dispatch(p, T, topk, H, _dtype_code(t[0]), int(bool(fp8)), _ptrs(t), _ptrs(s),
-                                     _ptrs(r), rows, _stream(t[0])), "vcoll_moe_dispatch")
+    _on_current_gpu(t[0])                         # every buffer shares its device
+    _apart(t, r, "vcoll_moe_dispatch")
+    table = lambda ts: (ctypes.c_void_p * len(ts))(*[x.data_ptr() or None for x in ts])            # noqa: E731
+    _check(_lib().vcoll_moe_dispatch(p, T, topk, H, _dtype_code(t[0]), int(bool(fp8)), table(t), table(s), table(r),
+                                     (ctypes.c_int64 * p)(*rr), _stream(t[0])), "vcoll_moe_dispatch")
     return recv
 
 

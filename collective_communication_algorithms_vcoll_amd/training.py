@@ -13,7 +13,9 @@ from __future__ import annotations
 
 import ctypes
 
-from . import BF16, F32, MAX_RANKS, _check, _disjoint, _lib, _no_overlap, _on_current_gpu, _ptrs, _stream
+import torch
+
+from . import BF16, F32, MAX_RANKS, _apart, _check, _lib, _on_current_gpu, _stream
 
 ADAMW_GROUP = 128          # elements per scale of an 8-bit state
 
@@ -55,64 +57,71 @@ _declare(_lib())
 
 
 def _first(x, what: str, name: str, dims: int):
-    """(p, shape of one rank's buffer, dtype, device) of per-rank buffers in either form."""
-    import torch
+    """(p, shape of one rank's buffer, one of the tensors) of per-rank buffers in either form."""
     if isinstance(x, torch.Tensor):
-        p, shape, t = (x.shape[0] if x.dim() else 0), tuple(x.shape[1:]), x
+        shape, t = tuple(x.shape), x
+        p, shape = (shape[0], shape[1:]) if shape else (0, ())
     else:
         p = len(x)
         if p == 0 or not isinstance(x[0], torch.Tensor):
             raise ValueError(f"{what}: {name} must be a tensor or a sequence of tensors, one per rank")
-        shape, t = tuple(x[0].shape), x[0]
+        t = x[0]
+        shape = tuple(t.shape)
     if not 1 <= p <= MAX_RANKS:
         raise ValueError(f"{what}: p={p} outside [1, {MAX_RANKS}]")
     if len(shape) != dims:
-        raise ValueError(f"{what}: {name} must have {dims} dimensions per rank, got {tuple(shape)}")
-    return p, shape, t.dtype, t.device
+        raise ValueError(f"{what}: {name} must have {dims} dimensions per rank, got {shape}")
+    return p, shape, t
+
+
+def _addresses(x, p: int):
+    """The addresses of the p rank buffers of a checked argument."""
+    if isinstance(x, torch.Tensor):
+        size = x.nbytes
+        if not size:
+            return (ctypes.c_void_p * p)()
+        base = x.data_ptr()
+        return (ctypes.c_void_p * p)(*range(base, base + size, size // p))
+    return (ctypes.c_void_p * p)(*[t.data_ptr() or None for t in x])
 
 
 def _table(x, p: int, shape: tuple, dtype, dev, what: str, name: str):
     """(addresses of the p rank buffers, the tensors behind them) after the checks."""
-    import torch
     if isinstance(x, torch.Tensor):
-        if tuple(x.shape) != (p, *shape) or x.dtype is not dtype or x.device != dev or not x.is_contiguous():
+        if x.shape != (p, *shape) or x.dtype is not dtype or x.device != dev or not x.is_contiguous():
             raise ValueError(f"{what}: {name} must be a contiguous {dtype} tensor {(p, *shape)} on {dev}, "
                              f"got {x.dtype} {tuple(x.shape)} on {x.device}")
-        if x.numel() == 0:
-            return (ctypes.c_void_p * p)(), []
-        step = x.numel() // p * x.element_size()
-        base = x.data_ptr()
-        return (ctypes.c_void_p * p)(*range(base, base + p * step, step)), [x]
-    ts = list(x)
-    if len(ts) != p:
-        raise ValueError(f"{what}: {name} must hold {p} rank buffers, got {len(ts)}")
-    for t in ts:
-        if tuple(t.shape) != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        return _addresses(x, p), [x]
+    if len(x) != p:
+        raise ValueError(f"{what}: {name} must hold {p} rank buffers, got {len(x)}")
+    for t in x:
+        if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{what}: every {name} must be a contiguous {dtype} tensor {shape} on {dev}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return (ctypes.c_void_p * p)(*[t.data_ptr() if t.numel() else None for t in ts]), ts
+    return _addresses(x, p), list(x)
 
 
 def _new(like, p: int, shape: tuple, dtype, dev):
-    """Rank buffers in the form of `like`."""
-    import torch
+    """New rank buffers in the form of `like`."""
     if isinstance(like, torch.Tensor):
         return torch.empty((p, *shape), dtype=dtype, device=dev)
     return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(p)]
 
 
-def _float_dtype(dtype, what: str) -> int:
-    import torch
+def _result(x, like, p: int, shape: tuple, dtype, dev, what: str, name: str):
+    """(rank buffers to write, their addresses, the given tensors): `x` after the checks, or new ones."""
+    if x is None:
+        x = _new(like, p, shape, dtype, dev)
+        return x, _addresses(x, p), []
+    return (x, *_table(x, p, shape, dtype, dev, what, name))
+
+
+def _float_code(dtype, what: str) -> int:
     if dtype is torch.float32:
         return F32
     if dtype is torch.bfloat16:
         return BF16
     raise TypeError(f"{what}: unsupported dtype {dtype}")
-
-
-def _any(x):
-    import torch
-    return x if isinstance(x, torch.Tensor) else x[0]
 
 
 # -----------------------------------------------------------------------------
@@ -123,49 +132,41 @@ def vcoll_moe_route(logits, topk: int, normalise: bool = True, ids=None, weights
     """Top-k experts and their softmax weights (see vcoll.h): logits [p,
     tokens, experts] float32 or bfloat16. Returns (ids [p, tokens, topk]
     int32, weights [p, tokens, topk] float32)."""
-    import torch
     what = "vcoll_moe_route"
-    p, (T, E), dt, dev = _first(logits, what, "logits", 2)
-    code = _float_dtype(dt, what)
+    p, (T, E), t = _first(logits, what, "logits", 2)
+    dev = t.device
+    code = _float_code(t.dtype, what)
     if not 1 <= topk <= E:
         raise ValueError(f"{what}: topk={topk} outside [1, {E}]")
-    z, zt = _table(logits, p, (T, E), dt, dev, what, "logits")
-    _on_current_gpu(_any(logits))
-    given = ids is not None or weights is not None
-    ids = _new(logits, p, (T, topk), torch.int32, dev) if ids is None else ids
-    weights = _new(logits, p, (T, topk), torch.float32, dev) if weights is None else weights
-    i, it = _table(ids, p, (T, topk), torch.int32, dev, what, "ids")
-    w, wt = _table(weights, p, (T, topk), torch.float32, dev, what, "weights")
-    if given:
-        _no_overlap(zt, it + wt, what)
-        _disjoint(it + wt, what)
-    _check(_lib().vcoll_moe_route(p, T, E, topk, code, int(bool(normalise)), z, i, w, _stream(_any(logits))), what)
+    z, zt = _table(logits, p, (T, E), t.dtype, dev, what, "logits")
+    _on_current_gpu(t)
+    ids, i, it = _result(ids, logits, p, (T, topk), torch.int32, dev, what, "ids")
+    weights, w, wt = _result(weights, logits, p, (T, topk), torch.float32, dev, what, "weights")
+    if it or wt:
+        _apart(zt, it + wt, what)
+    _check(_lib().vcoll_moe_route(p, T, E, topk, code, bool(normalise), z, i, w, _stream(t)), what)
     return ids, weights
 
 
 def vcoll_moe_route_backward(logits, ids, weights, d_weights, normalise: bool = True, d_logits=None):
     """Gradient of vcoll_moe_route's weights (see vcoll.h): d_weights [p,
     tokens, topk] float32. Returns d_logits like logits."""
-    import torch
     what = "vcoll_moe_route_backward"
-    p, (T, E), dt, dev = _first(logits, what, "logits", 2)
-    _, (_, K), _, _ = _first(ids, what, "ids", 2)
-    code = _float_dtype(dt, what)
+    p, (T, E), t = _first(logits, what, "logits", 2)
+    _, (_, K), _ = _first(ids, what, "ids", 2)
+    dev = t.device
+    code = _float_code(t.dtype, what)
     if not 1 <= K <= E:
         raise ValueError(f"{what}: topk={K} outside [1, {E}]")
-    z, zt = _table(logits, p, (T, E), dt, dev, what, "logits")
+    z, zt = _table(logits, p, (T, E), t.dtype, dev, what, "logits")
     i, it = _table(ids, p, (T, K), torch.int32, dev, what, "ids")
     w, wt = _table(weights, p, (T, K), torch.float32, dev, what, "weights")
     dw, dwt = _table(d_weights, p, (T, K), torch.float32, dev, what, "d_weights")
-    _on_current_gpu(_any(logits))
-    given = d_logits is not None
-    d_logits = d_logits if given else _new(logits, p, (T, E), dt, dev)
-    d, dtens = _table(d_logits, p, (T, E), dt, dev, what, "d_logits")
-    if given:
-        _no_overlap(zt + it + wt + dwt, dtens, what)
-        _disjoint(dtens, what)
-    _check(_lib().vcoll_moe_route_backward(p, T, E, K, code, int(bool(normalise)), z, i, w, dw, d,
-                                           _stream(_any(logits))), what)
+    _on_current_gpu(t)
+    d_logits, d, dt = _result(d_logits, logits, p, (T, E), t.dtype, dev, what, "d_logits")
+    if dt:
+        _apart(zt + it + wt + dwt, dt, what)
+    _check(_lib().vcoll_moe_route_backward(p, T, E, K, code, bool(normalise), z, i, w, dw, d, _stream(t)), what)
     return d_logits
 
 
@@ -186,32 +187,33 @@ def vcoll_moe_sort(ids, experts_per_rank: int, slots=None, offsets=None, workspa
     tokens, topk] int32. Returns (slots [p, tokens*topk, 2] int32 for
     vcoll_moe_dispatch and the combines, offsets [p, experts_per_rank + 1]
     int32). The workspace is made when None."""
-    import torch
     what = "vcoll_moe_sort"
-    p, (T, K), dt, dev = _first(ids, what, "ids", 2)
+    p, (T, K), t = _first(ids, what, "ids", 2)
+    dev = t.device
     if experts_per_rank < 1:
         raise ValueError(f"{what}: experts_per_rank={experts_per_rank} must be positive")
     i, it = _table(ids, p, (T, K), torch.int32, dev, what, "ids")
-    _on_current_gpu(_any(ids))
-    given = slots is not None or offsets is not None or workspace is not None
-    slots = _new(ids, p, (T * K, 2), torch.int32, dev) if slots is None else slots
-    offsets = torch.empty((p, experts_per_rank + 1), dtype=torch.int32, device=dev) if offsets is None else offsets
-    s, st = _table(slots, p, (T * K, 2), torch.int32, dev, what, "slots")
-    if tuple(offsets.shape) != (p, experts_per_rank + 1) or offsets.dtype is not torch.int32 or \
-            offsets.device != dev or not offsets.is_contiguous():
+    _on_current_gpu(t)
+    slots, s, written = _result(slots, ids, p, (T * K, 2), torch.int32, dev, what, "slots")
+    if offsets is None:
+        offsets = torch.empty((p, experts_per_rank + 1), dtype=torch.int32, device=dev)
+    elif offsets.shape != (p, experts_per_rank + 1) or offsets.dtype is not torch.int32 or offsets.device != dev or \
+            not offsets.is_contiguous():
         raise ValueError(f"{what}: offsets must be a contiguous int32 tensor {(p, experts_per_rank + 1)} on {dev}")
+    else:
+        written = written + [offsets]
     if workspace is None:
         need = vcoll_moe_sort_workspace(p, T, K, experts_per_rank)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"{what}: workspace must be a contiguous tensor on {dev}")
-    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    if given:
-        out = st + [offsets] + ([workspace] if size else [])
-        _no_overlap(it, out, what)
-        _disjoint(out, what)
+    else:
+        written = written + [workspace]
+    size = workspace.nbytes if workspace is not None else 0
+    if written:
+        _apart(it, written, what)
     _check(_lib().vcoll_moe_sort(p, T, K, experts_per_rank, i, s, offsets.data_ptr(),
-                                 workspace.data_ptr() if size else None, size, _stream(_any(ids))), what)
+                                 workspace.data_ptr() if size else None, size, _stream(t)), what)
     return slots, offsets
 
 
@@ -219,16 +221,18 @@ def vcoll_moe_sort(ids, experts_per_rank: int, slots=None, offsets=None, workspa
 # weighted combine
 
 
-def _expert_rows(expert, p: int, hidden, dtype, dev, what: str, name: str):
-    """(addresses, row counts, the tensors) of p buffers [rows_j, hidden]."""
-    ts = list(expert)
-    if len(ts) != p:
-        raise ValueError(f"{what}: {name} must hold {p} rank buffers, got {len(ts)}")
-    for t in ts:
-        if t.dim() != 2 or t.shape[1] != hidden or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+def _expert_rows(expert, p: int, hidden: int, dtype, dev, what: str, name: str):
+    """(addresses, row counts) of p buffers [rows_j, hidden]."""
+    if len(expert) != p:
+        raise ValueError(f"{what}: {name} must hold {p} rank buffers, got {len(expert)}")
+    rows = []
+    for t in expert:
+        shape = t.shape
+        if len(shape) != 2 or shape[1] != hidden or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{what}: every {name} must be a contiguous {dtype} tensor [rows, {hidden}] on {dev}, "
-                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return _ptrs(ts), (ctypes.c_int64 * p)(*[t.shape[0] for t in ts]), ts
+                             f"got {t.dtype} {tuple(shape)} on {t.device}")
+        rows.append(shape[0])
+    return _addresses(expert, p), rows
 
 
 def vcoll_moe_combine_weighted(expert_out, slots, weights, tokens: int, topk: int, out=None):
@@ -236,26 +240,23 @@ def vcoll_moe_combine_weighted(expert_out, slots, weights, tokens: int, topk: in
     tensors [rows_j, hidden]; slots [p, tokens*topk, 2] int32 of the dispatch;
     weights [p, tokens, topk] float32, or None for ones (the gradient of the
     dispatch). Returns out [p, tokens, hidden], in the form of slots."""
-    import torch
     what = "vcoll_moe_combine_weighted"
-    p, _, _, dev = _first(slots, what, "slots", 2)
-    T, K = int(tokens), int(topk)
-    first = expert_out[0]
-    if first.dim() != 2:
+    p, _, t = _first(slots, what, "slots", 2)
+    T, K, dev = int(tokens), int(topk), t.device
+    expert_out = list(expert_out)
+    if not expert_out or expert_out[0].dim() != 2:
         raise ValueError(f"{what}: expert_out must be [rows, hidden] per rank")
-    H, dt = first.shape[1], first.dtype
-    code = _float_dtype(dt, what)
+    H, dt = expert_out[0].shape[1], expert_out[0].dtype
+    code = _float_code(dt, what)
     s, st = _table(slots, p, (T * K, 2), torch.int32, dev, what, "slots")
     w, wt = (None, []) if weights is None else _table(weights, p, (T, K), torch.float32, dev, what, "weights")
-    _on_current_gpu(_any(slots))
-    e, rows, et = _expert_rows(expert_out, p, H, dt, dev, what, "expert_out")
-    given = out is not None
-    out = out if given else _new(slots, p, (T, H), dt, dev)
-    o, ot = _table(out, p, (T, H), dt, dev, what, "out")
-    if given:
-        _no_overlap(et + st + wt, ot, what)
-        _disjoint(ot, what)
-    _check(_lib().vcoll_moe_combine_weighted(p, T, K, H, code, e, rows, s, w, o, _stream(_any(slots))), what)
+    _on_current_gpu(t)
+    e, rows = _expert_rows(expert_out, p, H, dt, dev, what, "expert_out")
+    out, o, ot = _result(out, slots, p, (T, H), dt, dev, what, "out")
+    if ot:
+        _apart(expert_out + st + wt, ot, what)
+    _check(_lib().vcoll_moe_combine_weighted(p, T, K, H, code, e, (ctypes.c_int64 * p)(*rows), s, w, o, _stream(t)),
+           what)
     return out
 
 
@@ -265,29 +266,30 @@ def vcoll_moe_combine_weighted_backward(d_out, expert_out, slots, weights, topk:
     tokens, hidden]. Returns (d_expert_out, p tensors like expert_out;
     d_weights [p, tokens, topk] float32). Rows that no slot names are left as
     they are in a given d_expert_out and zero in one made here."""
-    import torch
     what = "vcoll_moe_combine_weighted_backward"
-    p, (T, H), dt, dev = _first(d_out, what, "d_out", 2)
-    K = int(topk)
-    code = _float_dtype(dt, what)
+    p, (T, H), t = _first(d_out, what, "d_out", 2)
+    K, dt, dev = int(topk), t.dtype, t.device
+    code = _float_code(dt, what)
     g, gt = _table(d_out, p, (T, H), dt, dev, what, "d_out")
     s, st = _table(slots, p, (T * K, 2), torch.int32, dev, what, "slots")
     w, wt = _table(weights, p, (T, K), torch.float32, dev, what, "weights")
-    _on_current_gpu(_any(d_out))
-    e, rows, et = _expert_rows(expert_out, p, H, dt, dev, what, "expert_out")
-    given = d_expert_out is not None or d_weights is not None
+    _on_current_gpu(t)
+    expert_out = list(expert_out)
+    e, rows = _expert_rows(expert_out, p, H, dt, dev, what, "expert_out")
+    written = []
     if d_expert_out is None:
-        d_expert_out = [torch.zeros_like(t) for t in et]
-    de, drows, det = _expert_rows(d_expert_out, p, H, dt, dev, what, "d_expert_out")
-    if list(drows) != list(rows):
-        raise ValueError(f"{what}: d_expert_out must have the rows of expert_out")
-    d_weights = _new(d_out, p, (T, K), torch.float32, dev) if d_weights is None else d_weights
-    dw, dwt = _table(d_weights, p, (T, K), torch.float32, dev, what, "d_weights")
-    if given:
-        _no_overlap(gt + st + wt + et, det + dwt, what)
-        _disjoint(det + dwt, what)
-    _check(_lib().vcoll_moe_combine_weighted_backward(p, T, K, H, code, g, e, rows, s, w, de, dw,
-                                                      _stream(_any(d_out))), what)
+        d_expert_out = [torch.zeros_like(x) for x in expert_out]
+        de = _addresses(d_expert_out, p)
+    else:
+        de, drows = _expert_rows(d_expert_out, p, H, dt, dev, what, "d_expert_out")
+        if drows != rows:
+            raise ValueError(f"{what}: d_expert_out must have the rows of expert_out")
+        written = list(d_expert_out)
+    d_weights, dw, dwt = _result(d_weights, d_out, p, (T, K), torch.float32, dev, what, "d_weights")
+    if written or dwt:
+        _apart(gt + st + wt + expert_out, written + dwt, what)
+    _check(_lib().vcoll_moe_combine_weighted_backward(p, T, K, H, code, g, e, (ctypes.c_int64 * p)(*rows), s, w, de, dw,
+                                                      _stream(t)), what)
     return d_expert_out, d_weights
 
 
@@ -299,7 +301,6 @@ def adamw_state(params, bits: int = 32):
     """Zero states for vcoll_adamw, as its keyword arguments: exp_avg and
     exp_avg_sq (float32, or 8-bit codes with their scales) and, for bfloat16
     parameters, the float32 master copies."""
-    import torch
     if bits not in (32, 8):
         raise ValueError(f"adamw_state: bits={bits} must be 32 or 8")
     ps = list(params)
@@ -336,15 +337,14 @@ def prepare_adamw(params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale
     does not run. params float32 or bfloat16 (then with float32 master
     copies), grads float32 or bfloat16, exp_avg and exp_avg_sq float32 or
     uint8 codes (then with float32 scales, one per 128 elements)."""
-    import torch
     what = "vcoll_adamw"
     ps = list(params)
     if not ps:
         return AdamwStep(None, 0, (F32, F32, 32), [])
     sides = [("params", ps), ("grads", list(grads)), ("exp_avg", list(exp_avg)), ("exp_avg_sq", list(exp_avg_sq))]
     dev = ps[0].device
-    pcode = _float_dtype(ps[0].dtype, what)
-    gcode = _float_dtype(sides[1][1][0].dtype, what) if sides[1][1] else F32
+    pcode = _float_code(ps[0].dtype, what)
+    gcode = _float_code(sides[1][1][0].dtype, what) if sides[1][1] else F32
     if not sides[2][1] or sides[2][1][0].dtype not in (torch.float32, torch.uint8):
         raise TypeError(f"{what}: exp_avg must be float32 or uint8 tensors")
     kind = sides[2][1][0].dtype
@@ -371,8 +371,7 @@ def prepare_adamw(params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale
                                  f"of {want} elements on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     _on_current_gpu(ps[0])
     written = [t for name, ts in sides + scales if name != "grads" for t in ts]
-    _disjoint(written, what)
-    _no_overlap(sides[1][1], written, what)
+    _apart(sides[1][1], written, what)
     columns = dict(sides + scales)
     table = (_AdamwTensor * len(ps))()
     fields = dict(param="params", grad="grads", master="master", exp_avg="exp_avg", exp_avg_sq="exp_avg_sq",
@@ -397,7 +396,6 @@ def vcoll_adamw(params, grads, exp_avg, exp_avg_sq, *, lr: float, step: int, mas
 def vcoll_adamw_unpack(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, exp_avg_out=None, exp_avg_sq_out=None):
     """The float32 values of one tensor's 8-bit AdamW states, as a checkpoint
     stores them. Returns (exp_avg, exp_avg_sq)."""
-    import torch
     what = "vcoll_adamw_unpack"
     n, dev = exp_avg.numel(), exp_avg.device
     groups = -(-n // ADAMW_GROUP)
@@ -411,7 +409,6 @@ def vcoll_adamw_unpack(exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, exp
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     _on_current_gpu(exp_avg)
     if given:
-        _no_overlap(list(ins), list(outs), what)
-        _disjoint(list(outs), what)
+        _apart(ins, outs, what)
     _check(_lib().vcoll_adamw_unpack(n, *[t.data_ptr() if n else None for t in ins + outs], _stream(exp_avg)), what)
     return exp_avg_out, exp_avg_sq_out
