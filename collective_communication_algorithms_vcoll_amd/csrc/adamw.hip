@@ -27,25 +27,22 @@ constexpr int kPer = 8;                            // elements per thread
 constexpr int kGroupLanes = kAdamwGroup / kPer;    // lanes that share a scale
 static_assert(kAdamwTile == kPer * kBlock, "one tile per workgroup");
 
-// 16-byte vectors of a buffer aligned to its elements only
-typedef u32x4 u32x4_e4 __attribute__((aligned(4)));
-typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x2 u32x2_e1 __attribute__((aligned(1)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ void load8(const float* p, float* f) {
-  Storage<VCOLL_F32>::widen(*reinterpret_cast<const u32x4_e4*>(p), f);
-  Storage<VCOLL_F32>::widen(*reinterpret_cast<const u32x4_e4*>(p + 4), f + 4);
+  Storage<VCOLL_F32>::widen(*reinterpret_cast<const u32x4_any*>(p), f);
+  Storage<VCOLL_F32>::widen(*reinterpret_cast<const u32x4_any*>(p + 4), f + 4);
 }
 __device__ __forceinline__ void load8(const uint16_t* p, float* f) {
-  Storage<VCOLL_BF16>::widen(*reinterpret_cast<const u32x4_e2*>(p), f);
+  Storage<VCOLL_BF16>::widen(*reinterpret_cast<const u32x4_any*>(p), f);
 }
 __device__ __forceinline__ void store8(float* p, const float* f) {
-  *reinterpret_cast<u32x4_e4*>(p) = Storage<VCOLL_F32>::narrow(f);
-  *reinterpret_cast<u32x4_e4*>(p + 4) = Storage<VCOLL_F32>::narrow(f + 4);
+  *reinterpret_cast<u32x4_any*>(p) = Storage<VCOLL_F32>::narrow(f);
+  *reinterpret_cast<u32x4_any*>(p + 4) = Storage<VCOLL_F32>::narrow(f + 4);
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float* f) {
-  *reinterpret_cast<u32x4_e2*>(p) = Storage<VCOLL_BF16>::narrow(f);
+  *reinterpret_cast<u32x4_any*>(p) = Storage<VCOLL_BF16>::narrow(f);
 }
 __device__ __forceinline__ float widen1(float x) { return x; }
 __device__ __forceinline__ float widen1(uint16_t x) { return Storage<VCOLL_BF16>::widen1(x); }
@@ -73,7 +70,7 @@ __device__ __forceinline__ void store_some(T* p, int live, const float* f) {
   }
 }
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int live) {
-  if (live == kPer) return *reinterpret_cast<const u32x2_e1*>(p);
+  if (live == kPer) return *reinterpret_cast<const u32x2_any*>(p);
   u32x2 w = {0, 0};
 #pragma unroll
   for (int c = 0; c < kPer; ++c)
@@ -82,7 +79,7 @@ __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int live) {
 }
 __device__ __forceinline__ void store_codes(uint8_t* p, int live, u32x2 w) {
   if (live == kPer) {
-    *reinterpret_cast<u32x2_e1*>(p) = w;
+    *reinterpret_cast<u32x2_any*>(p) = w;
   } else {
 #pragma unroll
     for (int c = 0; c < kPer; ++c)

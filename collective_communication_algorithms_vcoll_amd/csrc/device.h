@@ -13,6 +13,8 @@ namespace vcoll {
 namespace dev {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes in a buffer that is only aligned to its elements
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // ----------------------------------------------------------------------------
 // storage types: float32, or bfloat16 widened exactly and rounded once
