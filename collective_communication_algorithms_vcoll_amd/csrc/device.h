@@ -107,6 +107,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t raw_rsrc(const void* base, int
                                            kRawBufferFormat);
 }
 
+// Rotation of x by N lanes inside every row of 16 lanes.
+template <int N>
+__device__ __forceinline__ uint32_t rotate16(uint32_t x) {
+  return __builtin_amdgcn_mov_dpp(x, 0x120 + N, 0xf, 0xf, true);   // row_ror:N
+}
+
 template <int K, int N, class F>
 __device__ __forceinline__ void static_for(F&& f) {
   if constexpr (K < N) {

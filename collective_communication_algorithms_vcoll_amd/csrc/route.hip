@@ -19,11 +19,6 @@ using namespace dev;
 // lanes of one token: rotations inside rows of 16 lanes, shuffles beyond
 
 template <int N>
-__device__ __forceinline__ uint32_t rotate16(uint32_t x) {
-  return __builtin_amdgcn_mov_dpp(x, 0x120 + N, 0xf, 0xf, true);   // row_ror:N
-}
-
-template <int N>
 __device__ __forceinline__ float other(float x) {
   if constexpr (N >= 16) return __shfl_xor(x, N);
   else return __uint_as_float(rotate16<N>(__float_as_uint(x)));

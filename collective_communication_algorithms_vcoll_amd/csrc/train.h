@@ -83,7 +83,7 @@ static_assert(sizeof(WeightedBackwardArgs) <= 4096, "kernel arguments are limite
 
 constexpr int kAdamwTensors = 48;    // tensors described per launch
 constexpr int kAdamwGroup = 128;     // elements per scale of an 8-bit state
-constexpr int kAdamwTile = 2048;     // elements per workgroup, a multiple of the group
+constexpr int kAdamwTile = 1024;     // elements per workgroup, a multiple of the group
 
 struct AdamwTensor {
   int64_t n;
@@ -96,6 +96,8 @@ struct AdamwTensor {
   float* exp_avg_sq_scale;
   int32_t tile_start;                // first workgroup of this tensor
   uint32_t key;                      // of the tensor's random rounding
+  int32_t shift;                     // elements before the tensor in its first tile
+  int32_t pad;
 };
 
 struct AdamwArgs {

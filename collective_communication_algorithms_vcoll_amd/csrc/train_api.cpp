@@ -307,7 +307,11 @@ vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dty
   for (int k = 0; k < count; ++k) {
     const vcoll_adamw_tensor& t = tensors[k];
     if (t.n == 0) continue;
-    const int64_t more = (t.n + kAdamwTile - 1) / kAdamwTile;
+    // float32 states: tiles start on cache lines of the parameter, which the other buffers of a packed bucket share
+    // (8-bit ones start with the tensor, as its groups do)
+    const void* x = param_dtype == VCOLL_F32 ? t.param : t.master;
+    const int64_t shift = state_bits == 32 ? (reinterpret_cast<uintptr_t>(x) & 127u) / 4 : 0;
+    const int64_t more = (t.n + shift + kAdamwTile - 1) / kAdamwTile;
     if (a.count == kAdamwTensors || !grid_fits(tiles + more)) {
       const vcoll_status st = run();
       if (st != VCOLL_OK) return st;
@@ -322,6 +326,7 @@ vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dty
     d.exp_avg_scale = t.exp_avg_scale;
     d.exp_avg_sq_scale = t.exp_avg_sq_scale;
     d.tile_start = static_cast<int32_t>(tiles);
+    d.shift = static_cast<int32_t>(shift);
     d.key = mix32(first + 0x9E3779B9u * static_cast<uint32_t>(k));
     tiles += more;
   }

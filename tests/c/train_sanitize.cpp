@@ -57,7 +57,8 @@ hipError_t launch_adamw(const AdamwArgs& a, int32_t tiles, vcoll_dtype, vcoll_dt
   int64_t at = 0;
   for (int k = 0; k < a.count; ++k) {
     CHECK(a.t[k].tile_start == at && a.t[k].n > 0);
-    at += (a.t[k].n + kAdamwTile - 1) / kAdamwTile;
+    CHECK(a.t[k].shift >= 0 && a.t[k].shift < 32);
+    at += (a.t[k].n + a.t[k].shift + kAdamwTile - 1) / kAdamwTile;
     g_seen.push_back(a.t[k].param);
   }
   CHECK(at == tiles);
@@ -122,7 +123,7 @@ int main() {
     int live = 0;
     for (int k = 0; k < count; ++k) {
       t[k] = {k % 5 == 4 ? 0 : 1 + 777 * k, f[k], f[k], nullptr, f[k], f[k], nullptr, nullptr};
-      tiles += (t[k].n + 2047) / 2048;
+      tiles += (t[k].n + vcoll::kAdamwTile - 1) / vcoll::kAdamwTile;
       live += t[k].n > 0;
     }
     g_tiles = 0;
