@@ -18,6 +18,7 @@ using namespace dev;
 
 constexpr int kSortBlock = 1024;
 constexpr int kSortWaves = kSortBlock / 64;
+constexpr int kAhead = 4;            // steps of a wave whose loads are in flight together
 
 // Expert of pair n, or -1 for a pair without one.
 __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t n) {
@@ -26,26 +27,48 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t n) {
   return e >= 0 && e < a.experts ? e : -1;
 }
 
-// Counts the pairs of this workgroup's tile per wave and expert into
-// count[kSortWaves][experts].
-__device__ __forceinline__ void count_tile(const SortArgs& a, int32_t* count, uint32_t begin, uint32_t end) {
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+// Experts of up to kAhead steps of this wave, from pair `begin` of its run on:
+// their loads are in flight together.
+__device__ __forceinline__ void experts_ahead(const SortArgs& a, uint32_t begin, uint32_t end, int* e) {
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) {
+    const uint32_t n = begin + 64 * s + threadIdx.x % 64;
+    e[s] = n < end ? expert_of(a, n) : -1;
+  }
+}
+
+// The pairs of this wave: its run of the workgroup's tile.
+struct Run {
+  uint32_t begin, end;
+};
+__device__ __forceinline__ Run run_of(const SortArgs& a) {
+  const uint32_t size = a.tile / kSortWaves;
+  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(a.tile) + threadIdx.x / 64 * size;
+  return {begin, min(begin + size, static_cast<uint32_t>(a.pairs))};
+}
+
+// Counts this wave's pairs per expert into count[wave][experts]; e holds the
+// experts of the run's last kAhead steps, all of a run of that many.
+__device__ __forceinline__ void count_tile(const SortArgs& a, int32_t* count, const Run run, int* e) {
+  experts_ahead(a, run.begin, run.end, e);
   for (int x = threadIdx.x; x < kSortWaves * a.experts; x += kSortBlock) count[x] = 0;
   __syncthreads();
-  const uint32_t run = a.tile / kSortWaves;
-  for (uint32_t s = 0; s < run; s += 64) {
-    const uint32_t n = begin + wave * run + s + lane;
-    const int e = n < end ? expert_of(a, n) : -1;
-    if (e >= 0) atomicAdd(&count[wave * a.experts + e], 1);
+  int32_t* mine = count + threadIdx.x / 64 * a.experts;
+  for (uint32_t n = run.begin;;) {
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+      if (e[s] >= 0) atomicAdd(&mine[e[s]], 1);
+    n += 64 * kAhead;
+    if (n >= run.end) break;
+    experts_ahead(a, n, run.end, e);
   }
   __syncthreads();
 }
 
 __global__ __launch_bounds__(kSortBlock) void sort_count_kernel(const SortArgs a) {
   extern __shared__ int32_t count[];
-  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(a.tile);
-  const uint32_t end = min(begin + static_cast<uint32_t>(a.tile), static_cast<uint32_t>(a.pairs));
-  count_tile(a, count, begin, end);
+  int ahead[kAhead];
+  count_tile(a, count, run_of(a), ahead);
   for (int e = threadIdx.x; e < a.experts; e += kSortBlock) {
     int32_t sum = 0;
 #pragma unroll
@@ -58,23 +81,39 @@ __global__ __launch_bounds__(kSortBlock) void sort_place_kernel(const SortArgs a
   extern __shared__ int32_t next[];                       // [kSortWaves][experts]
   __shared__ int32_t scan[kSortBlock + 1];                // pairs of all experts before e
   __shared__ int32_t wave_total[kSortWaves];
+  __shared__ int2 part[kSortBlock];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-  const uint32_t begin = blockIdx.x * static_cast<uint32_t>(a.tile);
-  const uint32_t end = min(begin + static_cast<uint32_t>(a.tile), static_cast<uint32_t>(a.pairs));
-  count_tile(a, next, begin, end);
+  const Run run = run_of(a);
+  int ahead[kAhead];
+  count_tile(a, next, run, ahead);
 
   // thread e: pairs of expert e in all tiles, and in the tiles before this one
   int32_t total = 0, before = 0;
-  if (tid < a.experts) {
-    if (a.blocks == 1) {
+  if (a.blocks == 1) {
+    if (tid < a.experts) {
 #pragma unroll
       for (int w = 0; w < kSortWaves; ++w) total += next[w * a.experts + tid];
-    } else {
+    }
+  } else {
+    // `groups` threads share an expert's column of the counts
+    const int wide = 1 << (32 - __clz(a.experts - 1 | 63));
+    const int groups = kSortBlock / wide;
+    const int e = tid & (wide - 1);
+    if (e < a.experts) {
 #pragma unroll 8
-      for (int b = 0; b < a.blocks; ++b) {
-        const int32_t c = a.counts[static_cast<int64_t>(b) * a.experts + tid];
+      for (int b = tid / wide; b < a.blocks; b += groups) {
+        const int32_t c = a.counts[static_cast<int64_t>(b) * a.experts + e];
         total += c;
         before += b < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+    }
+    part[tid] = {total, before};
+    __syncthreads();
+    total = before = 0;
+    if (tid < a.experts) {
+      for (int g = 0; g < groups; ++g) {
+        total += part[g * wide + tid].x;
+        before += part[g * wide + tid].y;
       }
     }
   }
@@ -108,29 +147,30 @@ __global__ __launch_bounds__(kSortBlock) void sort_place_kernel(const SortArgs a
   }
   __syncthreads();
 
-  const uint32_t run = a.tile / kSortWaves;
-  for (uint32_t s = 0; s < run; s += 64) {
-    const uint32_t n = begin + wave * run + s + lane;
-    const int e = n < end ? expert_of(a, n) : -1;
-    uint64_t same = __ballot(e >= 0);
-    for (int bit = 1; bit < a.experts; bit <<= 1) {
-      const uint64_t ones = __ballot((e & bit) != 0);
-      same &= (e & bit) ? ones : ~ones;
-    }
-    int32_t row = -1, rank = -1;
-    const int leader = e >= 0 ? __ffsll(static_cast<unsigned long long>(same)) - 1 : lane;
-    int32_t at = 0;
-    if (e >= 0 && lane == leader) at = atomicAdd(&next[wave * a.experts + e], __popcll(same));
-    at = __shfl(at, leader);
-    if (e >= 0) {
-      rank = e / a.experts_per_rank;
-      row = at + __popcll(same & ((uint64_t(1) << lane) - 1));
-    }
-    if (n < end) {
-      const uint32_t i = n / static_cast<uint32_t>(a.pairs_per_rank);
-      int32_t* slot = a.slots[i] + 2 * static_cast<int64_t>(n - i * a.pairs_per_rank);
-      slot[0] = rank;
-      slot[1] = row;
+  for (uint32_t n0 = run.begin; n0 < run.end; n0 += 64 * kAhead) {
+    if (run.end - run.begin > 64 * kAhead) experts_ahead(a, n0, run.end, ahead);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const uint32_t n = n0 + 64 * s + lane;
+      const int e = ahead[s];
+      uint64_t same = __ballot(e >= 0);
+      if (same == 0 && n0 + 64 * s >= run.end) break;
+      for (int bit = 1; bit < a.experts; bit <<= 1) {
+        const uint64_t ones = __ballot((e & bit) != 0);
+        same &= (e & bit) ? ones : ~ones;
+      }
+      int32_t row = -1, rank = -1, at = 0;
+      const int leader = e >= 0 ? __ffsll(static_cast<unsigned long long>(same)) - 1 : lane;
+      if (e >= 0 && lane == leader) at = atomicAdd(&next[wave * a.experts + e], __popcll(same));
+      at = __shfl(at, leader);
+      if (e >= 0) {
+        rank = e / a.experts_per_rank;
+        row = at + __popcll(same & ((uint64_t(1) << lane) - 1));
+      }
+      if (n < run.end) {
+        const uint32_t i = n / static_cast<uint32_t>(a.pairs_per_rank);
+        reinterpret_cast<int2*>(a.slots[i])[n - i * a.pairs_per_rank] = {rank, row};
+      }
     }
   }
 }

@@ -40,13 +40,15 @@ vcoll_status by_ranks(int p, F&& run) {
   return VCOLL_OK;
 }
 
-// Tiles of the expert sort: at most kSortTiles, each a whole number of steps
-// of its 16 waves.
+// Tiles of the expert sort, each a whole number of steps of its 16 waves.
+// Every tile reads the counts of all of them, so more experts take fewer,
+// larger tiles: 32768 counts, 64 to 256 tiles (8 x 4096 tokens, top 8 of 256,
+// on MI355X: 12.3 us with 128 tiles, 13.4 with 256, 14.0 with 64).
 constexpr int64_t kSortStep = 1024;
-constexpr int64_t kSortTiles = 256;
 
-int64_t sort_tile(int64_t pairs) {
-  const int64_t per = (pairs + kSortTiles - 1) / kSortTiles;
+int64_t sort_tile(int64_t pairs, int64_t experts) {
+  const int64_t tiles = std::min<int64_t>(256, std::max<int64_t>(64, 32768 / experts));
+  const int64_t per = (pairs + tiles - 1) / tiles;
   return std::max<int64_t>(1, (per + kSortStep - 1) / kSortStep) * kSortStep;
 }
 
@@ -55,10 +57,13 @@ bool valid_sort(int p, int64_t tokens, int topk, int experts_per_rank) {
          tokens * topk <= INT32_MAX / p;
 }
 
-int64_t sort_blocks(int64_t pairs) { return std::max<int64_t>(1, (pairs + sort_tile(pairs) - 1) / sort_tile(pairs)); }
+int64_t sort_blocks(int64_t pairs, int64_t experts) {
+  const int64_t tile = sort_tile(pairs, experts);
+  return std::max<int64_t>(1, (pairs + tile - 1) / tile);
+}
 
 int64_t sort_bytes(int64_t pairs, int64_t experts) {
-  const int64_t blocks = sort_blocks(pairs);
+  const int64_t blocks = sort_blocks(pairs, experts);
   return blocks > 1 ? blocks * experts * 4 : 0;
 }
 
@@ -180,8 +185,8 @@ vcoll_status vcoll_moe_sort(int p, int64_t tokens, int topk, int experts_per_ran
   a.experts = p * experts_per_rank;
   a.pairs_per_rank = static_cast<int32_t>(tokens * topk);
   a.pairs = static_cast<int32_t>(pairs);
-  a.tile = static_cast<int32_t>(sort_tile(pairs));
-  a.blocks = static_cast<int32_t>(sort_blocks(pairs));
+  a.tile = static_cast<int32_t>(sort_tile(pairs, a.experts));
+  a.blocks = static_cast<int32_t>(sort_blocks(pairs, a.experts));
   return from_hip(launch_sort(a, static_cast<hipStream_t>(stream)));
 }
 
