@@ -255,6 +255,29 @@ def test_sorted_rows_through_the_dispatch(vc):
             assert torch.equal(recv[j][got[j][l]:got[j][l + 1]], want), (j, l)
 
 
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("H,off", [(1, 0), (3, 0), (8, 0), (24, 0), (72, 1), (144, 0), (500, 0), (1001, 0), (1024, 0),
+                                   (1032, 3), (2639, 0), (4096, 0), (4100, 1)])
+def test_dispatch_rows_of_any_width(vc, name, H, off):
+    """Short, odd and unaligned rows (the last receive rows untouched): the same bytes as indexing."""
+    import torch
+    p, T, K, per_rank = 3, 21, 5, 4
+    ids = expert_ids(p, T, K, p * per_rank, H)
+    slots, offsets = train.expert_sort(ids, per_rank)
+
+    def flat(n):
+        return torch.full((n + off,), 7.0, device="cuda", dtype=dt(name))[off:]
+    x = [flat(T * H).view(T, H).copy_(torch.randn((T, H), device="cuda")) for _ in range(p)]
+    rows = [int(offsets[j, -1]) for j in range(p)]
+    recv = [flat((n + 1) * H).view(n + 1, H) for n in rows]
+    vc.vcoll_moe_dispatch(x, [put_ids(s) for s in slots], rows, K, recv=recv)
+    for i in range(p):
+        for n, (j, r) in enumerate(slots[i]):
+            if j >= 0:
+                assert torch.equal(recv[j][r], x[i][n // K]), (i, n)
+    assert all(bool((recv[j][rows[j]] == 7).all()) for j in range(p))
+
+
 # --- weighted combine ---------------------------------------------------------------
 
 def experts_case(p, T, K, H, per_rank, name, seed, gone=0.2, spare=2):

@@ -360,6 +360,27 @@ def test_binding_refuses_wrong_buffers():
             f()
 
 
+def test_overlap_sweep_agrees_with_pairwise_comparison():
+    import torch
+    flat = torch.zeros(64, dtype=torch.uint8)
+    rng = np.random.default_rng(1)
+    seen = set()
+    for _ in range(4000):
+        span = lambda: (lambda a, n: flat[a:a + n])(*(int(x) for x in rng.integers(0, (56, 9))))   # noqa: E731
+        ins, outs = [span() for _ in range(rng.integers(0, 4))], [span() for _ in range(rng.integers(0, 4))]
+        meet = lambda x, y: x.numel() and y.numel() and x.data_ptr() < y.data_ptr() + y.numel() \
+            and y.data_ptr() < x.data_ptr() + x.numel()                                           # noqa: E731
+        want = any(meet(x, y) for k, x in enumerate(outs) for y in outs[k + 1:] + ins)
+        try:
+            vc._apart(ins, outs, "test")
+            got = False
+        except ValueError:
+            got = True
+        assert got == bool(want)
+        seen.add(got)
+    assert seen == {True, False}
+
+
 def test_binding_steps_over_no_tensors():
     vc.vcoll_adamw([], [], [], [], lr=1e-3, step=1)
 
