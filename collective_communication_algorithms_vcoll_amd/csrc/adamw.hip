@@ -60,8 +60,8 @@ __device__ __forceinline__ void store4(float* p, const float* f) {
 }
 __device__ __forceinline__ void store4(uint16_t* p, const float* f) {
   u32x2 w;
-  w.x = bf16_rne(f[0]) | (bf16_rne(f[1]) << 16);
-  w.y = bf16_rne(f[2]) | (bf16_rne(f[3]) << 16);
+  w.x = pack_bf16(f[0], f[1]);
+  w.y = pack_bf16(f[2], f[3]);
   store_v<u32x2_any>(p, w);
 }
 __device__ __forceinline__ float widen1(float x) { return x; }

@@ -28,6 +28,14 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) {
   return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
+// The same rounding of two values by gfx950's packed conversion (NaN stays a
+// quiet NaN), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 template <int D>
 struct Storage;
 
@@ -78,6 +86,15 @@ struct Storage<VCOLL_BF16> {
   __device__ static __forceinline__ float widen1(elem e) { return __uint_as_float(uint32_t(e) << 16); }
   __device__ static __forceinline__ elem narrow1(float f) { return static_cast<elem>(bf16_rne(f)); }
 };
+
+// 16 bytes of storage elements from float32, rounded as Storage::narrow does.
+template <int D>
+__device__ __forceinline__ u32x4 narrow16(const float* f) {
+  if constexpr (D == VCOLL_BF16)
+    return {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+  else
+    return Storage<D>::narrow(f);
+}
 
 // ----------------------------------------------------------------------------
 // memory access: 16-byte vectors, streamed (each byte is touched once)

@@ -16,36 +16,39 @@ namespace {
 using namespace dev;
 
 // ----------------------------------------------------------------------------
-// lanes of one token: rotations inside rows of 16 lanes, shuffles beyond
+// lanes of one token
 
-template <int N>
-__device__ __forceinline__ float other(float x) {
-  if constexpr (N >= 16) return __shfl_xor(x, N);
-  else return __uint_as_float(rotate16<N>(__float_as_uint(x)));
+__device__ __forceinline__ float rotated(float x, uint32_t (*by)(uint32_t)) { return __uint_as_float(by(__float_as_uint(x))); }
+
+__device__ __forceinline__ double rotated(double x, uint32_t (*by)(uint32_t)) {
+  const uint64_t u = __double_as_longlong(x);
+  return __longlong_as_double((static_cast<uint64_t>(by(static_cast<uint32_t>(u >> 32))) << 32) |
+                              by(static_cast<uint32_t>(u)));
 }
 
-template <int N>
-__device__ __forceinline__ double other(double x) {
-  if constexpr (N >= 16) {
-    return __shfl_xor(x, N);
-  } else {
-    const uint64_t u = __double_as_longlong(x);
-    const uint64_t r = (static_cast<uint64_t>(rotate16<N>(static_cast<uint32_t>(u >> 32))) << 32) |
-                       rotate16<N>(static_cast<uint32_t>(u));
-    return __longlong_as_double(r);
-  }
+__device__ __forceinline__ float of_lane(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
 }
 
-// Reductions whose result is the same in all L lanes (of a sum too: the pairs
-// that two lanes add differ in order only).
+__device__ __forceinline__ double of_lane(double x, int lane) {
+  const uint64_t u = __double_as_longlong(x);
+  const uint32_t high = __builtin_amdgcn_readlane(static_cast<uint32_t>(u >> 32), lane);
+  const uint32_t low = __builtin_amdgcn_readlane(static_cast<uint32_t>(u), lane);
+  return __longlong_as_double((static_cast<uint64_t>(high) << 32) | low);
+}
+
+// Reductions over the L lanes of a token, the same in all of them (of a sum
+// too: the pairs that two lanes add differ in order only). Rows of 16 lanes
+// join by rotations, the four rows of a wave by reading one lane of each.
 template <int L, class T, class F>
 __device__ __forceinline__ T across(T x, F&& join) {
-  if constexpr (L > 32) x = join(x, other<32>(x));
-  if constexpr (L > 16) x = join(x, other<16>(x));
-  x = join(x, other<8>(x));
-  x = join(x, other<4>(x));
-  x = join(x, other<2>(x));
-  return join(x, other<1>(x));
+  static_assert(L == 16 || L == 64, "a row or a wave");
+  x = join(x, rotated(x, rotate16<8>));
+  x = join(x, rotated(x, rotate16<4>));
+  x = join(x, rotated(x, rotate16<2>));
+  x = join(x, rotated(x, rotate16<1>));
+  if constexpr (L == 64) x = join(join(of_lane(x, 0), of_lane(x, 16)), join(of_lane(x, 32), of_lane(x, 48)));
+  return x;
 }
 
 template <int L>
@@ -102,7 +105,7 @@ __device__ __forceinline__ void store_logits(void* row, int experts, int lane, c
     for (int v = 0; v < V; v += S::kVE) {
       const int e = expert_at<D, L, V, VEC>(lane, v);
       if (e < experts)
-        __builtin_nontemporal_store(S::narrow(d + v), reinterpret_cast<u32x4_any*>(static_cast<E*>(row) + e));
+        __builtin_nontemporal_store(narrow16<D>(d + v), reinterpret_cast<u32x4_any*>(static_cast<E*>(row) + e));
     }
   } else {
 #pragma unroll
@@ -167,10 +170,70 @@ __device__ __forceinline__ void sort_descending(double* key) {
   });
 }
 
-// Every lane sorts its V keys once; a round takes the largest head over the
-// token's lanes and moves that lane's list up. W: how much of its list a lane
-// can need (topk <= W, or W = V).
-template <int D, int L, int V, int W, bool VEC>
+// The 8 largest of two descending lists of 8, descending, into a: the larger
+// of a[i] and b[7 - i] are those 8 in bitonic order.
+__device__ __forceinline__ void merge8(double* a, const double* b) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = __builtin_fmax(a[i], b[7 - i]);
+  static_for<0, 3>([&](auto s) {
+    constexpr int d = 4 >> decltype(s)::value;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & d) == 0) {
+        const double x = a[i], y = a[i + d];
+        a[i] = __builtin_fmax(x, y);
+        a[i + d] = __builtin_fmin(x, y);
+      }
+    }
+  });
+}
+
+// merge8 with the list of the lane N before in the row.
+template <int N>
+__device__ __forceinline__ void merge_rotated(double* a) {
+  double b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = rotated(a[i], rotate16<N>);
+  merge8(a, b);
+}
+
+// The 8 largest keys of a token's z over a row of lanes, descending and the
+// same in all of them. A lane sorts its keys 8 at a time and merges the
+// lists, then the lanes' lists merge pairwise.
+template <int D, int V, bool VEC>
+__device__ __forceinline__ void largest8(const float* z, int lane, double* list) {
+  static_assert(V % 8 == 0, "whole lists");
+#pragma unroll
+  for (int v = 0; v < V; v += 8) {
+    double key[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) key[c] = key_of(z[v + c], expert_at<D, 16, V, VEC>(lane, v + c));
+    sort_descending<8>(key);
+    if (v == 0) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) list[c] = key[c];
+    } else {
+      merge8(list, key);
+    }
+  }
+  merge_rotated<8>(list);
+  merge_rotated<4>(list);
+  merge_rotated<2>(list);
+  merge_rotated<1>(list);
+}
+
+// MERGE (up to 8 chosen, 16 lanes): largest8. Otherwise every lane sorts its
+// keys, and a round for each chosen expert takes the largest head over the
+// token's lanes and moves that lane's list up. A lane keeps the C chosen keys
+// lane, lane + L, ..
+//
+// 8 x 4096 tokens, top 8, on MI355X: of 256 float32 logits 11.4 us merged and
+// 13.2 in rounds, of 512 17.8 and 32.1, of 1024 bf16 ones 31.7 and 45.9 (in
+// rounds over a whole wave); top 20 of 128 in rounds 16.5 us over rows, 40
+// over waves. One wave per token with its maximum taken over all logits in
+// every round took 45 us for 256. The instructions of the selection bound it,
+// not its bytes (5.6 us).
+template <int D, int L, int V, int C, bool MERGE, bool VEC>
 __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
   using E = typename Storage<D>::elem;
   const int lane = threadIdx.x % L;
@@ -179,27 +242,48 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
   const bool live = t < a.tokens;
   float z[V];
   load_logits<D, L, V, VEC>(static_cast<const E*>(a.logits[i]) + t * a.experts, a.experts, lane, live, z);
-  double key[V];
+  double chosen[C], first = 0.0;
+  if constexpr (MERGE) {
+    static_assert(L == 16 && C == 1, "one row, one chosen key per lane");
+    double list[8];
+    largest8<D, V, VEC>(z, lane, list);
+    first = list[0];
+    chosen[0] = list[0];
 #pragma unroll
-  for (int v = 0; v < V; ++v) key[v] = key_of(z[v], expert_at<D, L, V, VEC>(lane, v));
-  sort_descending<V>(key);
-  double chosen = 0.0, first = 0.0;
-  for (int k = 0; k < a.topk; ++k) {
-    const double best = across<L>(key[0], [](double x, double y) { return __builtin_fmax(x, y); });
-    if (k == 0) first = best;
-    if (lane == k) chosen = best;
-    const bool mine = key[0] == best;
-#pragma unroll
-    for (int w = 0; w + 1 < W; ++w) {
-      const double here = key[w], next = key[w + 1];
-      key[w] = mine ? next : here;
+    for (int k = 1; k < 8; ++k) {
+      const double next = list[k], kept = chosen[0];
+      chosen[0] = lane == k ? next : kept;
     }
-    key[W - 1] = mine ? 0.0 : key[W - 1];
+  } else {
+    double key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key_of(z[v], expert_at<D, L, V, VEC>(lane, v));
+    sort_descending<V>(key);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      chosen[c] = 0.0;
+      for (int k = 0; k < L && c * L + k < a.topk; ++k) {
+        const double best = across<L>(key[0], [](double x, double y) { return __builtin_fmax(x, y); });
+        if (c == 0 && k == 0) first = best;
+        if (lane == k) chosen[c] = best;
+        const bool mine = key[0] == best;
+#pragma unroll
+        for (int v = 0; v + 1 < V; ++v) {
+          const double here = key[v], next = key[v + 1];
+          key[v] = mine ? next : here;
+        }
+        key[V - 1] = mine ? 0.0 : key[V - 1];
+      }
+    }
   }
-  const bool taken = chosen >= 1.0;
   const float peak = key_logit(first);
-  const float mine = taken ? exp_of(key_logit(chosen) - peak) : 0.0f;
-  float total = mine;
+  float total = 0.0f, mine[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const bool taken = lane + c * L < a.topk && chosen[c] >= 1.0;
+    mine[c] = taken ? exp_of(key_logit(chosen[c]) - peak) : 0.0f;
+    total += mine[c];
+  }
   if (!a.normalise) {
     total = 0.0f;
 #pragma unroll
@@ -207,14 +291,19 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const RouteArgs a) {
       total += expert_at<D, L, V, VEC>(lane, v) < a.experts ? exp_of(z[v] - peak) : 0.0f;
   }
   total = sum_across<L>(total);
-  if (live && lane < a.topk) {
-    a.ids[i][t * a.topk + lane] = taken ? key_expert(chosen) : -1;
-    a.weights[i][t * a.topk + lane] = taken ? mine / total : 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k = lane + c * L;
+    if (live && k < a.topk) {
+      const bool taken = chosen[c] >= 1.0;
+      a.ids[i][t * a.topk + k] = taken ? key_expert(chosen[c]) : -1;
+      a.weights[i][t * a.topk + k] = taken ? mine[c] / total : 0.0f;
+    }
   }
 }
 
 // The topk gradient terms reach their experts' lanes through a float row in LDS.
-template <int D, int L, int V, bool VEC>
+template <int D, int L, int V, int C, bool VEC>
 __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteBackwardArgs a) {
   using E = typename Storage<D>::elem;
   __shared__ float row[kBlock / L][L * V];
@@ -222,24 +311,33 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteBackw
   const int i = blockIdx.y;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock / L) + token;
   const bool live = t < a.tokens;
-  int id = -1;
-  float w = 0.0f, dw = 0.0f;
-  if (live && lane < a.topk) {
-    id = a.ids[i][t * a.topk + lane];
-    if (id < 0 || id >= a.experts) id = -1;
-    if (id >= 0) {
-      w = a.weights[i][t * a.topk + lane];
-      dw = a.d_weights[i][t * a.topk + lane];
+  int id[C];
+  float w[C], dw[C], mean = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k = lane + c * L;
+    id[c] = -1;
+    w[c] = dw[c] = 0.0f;
+    if (live && k < a.topk) {
+      id[c] = a.ids[i][t * a.topk + k];
+      if (id[c] < 0 || id[c] >= a.experts) id[c] = -1;
+      if (id[c] >= 0) {
+        w[c] = a.weights[i][t * a.topk + k];
+        dw[c] = a.d_weights[i][t * a.topk + k];
+      }
     }
+    mean += w[c] * dw[c];
   }
   float z[V];
   if (!a.normalise)
     load_logits<D, L, V, VEC>(static_cast<const E*>(a.logits[i]) + t * a.experts, a.experts, lane, live, z);
 #pragma unroll
   for (int v = 0; v < V; ++v) row[token][lane + L * v] = 0.0f;
-  const float mean = sum_across<L>(w * dw);
+  mean = sum_across<L>(mean);
   __syncthreads();
-  if (id >= 0) row[token][id] = a.normalise ? w * (dw - mean) : dw;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (id[c] >= 0) row[token][id[c]] = a.normalise ? w[c] * (dw[c] - mean) : dw[c];
   __syncthreads();
   float d[V];
 #pragma unroll
@@ -264,19 +362,19 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(const RouteBackw
 }
 
 // ----------------------------------------------------------------------------
-// launch: 16 lanes per token where they hold its logits and its chosen
-// experts, else the whole wave
+// launch: a row of 16 lanes per token, or the whole wave where a row could
+// not hold the logits
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 template <class F>
-hipError_t by_shape(int experts, int topk, F&& run) {
-  using std::integral_constant;
-  if (topk <= 16 && experts <= 64) return run(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-  if (topk <= 16 && experts <= 128) return run(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-  if (topk <= 16 && experts <= 256) return run(integral_constant<int, 16>{}, integral_constant<int, 16>{});
-  if (experts <= 64) return run(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (experts <= 256) return run(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  if (experts <= 512) return run(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-  return run(integral_constant<int, 64>{}, integral_constant<int, kMaxExperts / 64>{});
+hipError_t by_shape(int experts, F&& run) {
+  if (experts <= 64) return run(Int<16>{}, Int<4>{});
+  if (experts <= 128) return run(Int<16>{}, Int<8>{});
+  if (experts <= 256) return run(Int<16>{}, Int<16>{});
+  if (experts <= 512) return run(Int<64>{}, Int<8>{});
+  return run(Int<64>{}, Int<kMaxExperts / 64>{});
 }
 
 template <int L>
@@ -285,30 +383,52 @@ dim3 token_grid(int64_t tokens, int ranks) {
   return dim3(static_cast<unsigned>((tokens + per - 1) / per), ranks);
 }
 
+template <int D, int V>
+hipError_t launch_route_merged(const RouteArgs& a, hipStream_t stream) {
+  if (a.experts % Storage<D>::kVE == 0)
+    return launch(route_kernel<D, 16, V, 1, true, true>, token_grid<16>(a.tokens, a.ranks), a, stream);
+  return launch(route_kernel<D, 16, V, 1, true, false>, token_grid<16>(a.tokens, a.ranks), a, stream);
+}
+
+template <int D, int L, int V, bool VEC>
+hipError_t launch_route_rounds(const RouteArgs& a, hipStream_t stream) {
+  if constexpr (L < kMaxTopk)
+    if (a.topk > L)
+      return launch(route_kernel<D, L, V, kMaxTopk / L, false, VEC>, token_grid<L>(a.tokens, a.ranks), a, stream);
+  return launch(route_kernel<D, L, V, 1, false, VEC>, token_grid<L>(a.tokens, a.ranks), a, stream);
+}
+
 template <int D>
 hipError_t launch_route_dt(const RouteArgs& a, hipStream_t stream) {
-  return by_shape(a.experts, a.topk, [&](auto l, auto v) {
+  if (a.topk <= 8 && a.experts > 64) {
+    if (a.experts <= 128) return launch_route_merged<D, 8>(a, stream);
+    if (a.experts <= 256) return launch_route_merged<D, 16>(a, stream);
+    if (a.experts <= 512) return launch_route_merged<D, 32>(a, stream);
+    return launch_route_merged<D, kMaxExperts / 16>(a, stream);
+  }
+  return by_shape(a.experts, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value, VE = Storage<D>::kVE;
-    const dim3 grid = token_grid<L>(a.tokens, a.ranks);
-    if constexpr (V % VE == 0) {
-      if (a.experts % VE == 0) {
-        if constexpr (V > 8)
-          if (a.topk <= 8) return launch(route_kernel<D, L, V, 8, true>, grid, a, stream);
-        return launch(route_kernel<D, L, V, V, true>, grid, a, stream);
-      }
-    }
-    return launch(route_kernel<D, L, V, V, false>, grid, a, stream);
+    if constexpr (V % VE == 0)
+      if (a.experts % VE == 0) return launch_route_rounds<D, L, V, true>(a, stream);
+    return launch_route_rounds<D, L, V, false>(a, stream);
   });
+}
+
+template <int D, int L, int V, bool VEC>
+hipError_t launch_route_backward_vec(const RouteBackwardArgs& a, hipStream_t stream) {
+  if constexpr (L < kMaxTopk)
+    if (a.topk > L)
+      return launch(route_backward_kernel<D, L, V, kMaxTopk / L, VEC>, token_grid<L>(a.tokens, a.ranks), a, stream);
+  return launch(route_backward_kernel<D, L, V, 1, VEC>, token_grid<L>(a.tokens, a.ranks), a, stream);
 }
 
 template <int D>
 hipError_t launch_route_backward_dt(const RouteBackwardArgs& a, hipStream_t stream) {
-  return by_shape(a.experts, a.topk, [&](auto l, auto v) {
+  return by_shape(a.experts, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value, VE = Storage<D>::kVE;
-    const dim3 grid = token_grid<L>(a.tokens, a.ranks);
     if constexpr (V % VE == 0)
-      if (a.experts % VE == 0) return launch(route_backward_kernel<D, L, V, true>, grid, a, stream);
-    return launch(route_backward_kernel<D, L, V, false>, grid, a, stream);
+      if (a.experts % VE == 0) return launch_route_backward_vec<D, L, V, true>(a, stream);
+    return launch_route_backward_vec<D, L, V, false>(a, stream);
   });
 }
 

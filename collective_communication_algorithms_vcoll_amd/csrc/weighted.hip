@@ -24,15 +24,17 @@ namespace {
 
 using namespace dev;
 
+
 // Expert rows are read once and written once, so both stream past the caches.
 // On MI355X, with the rows of 8 x 4096 tokens x 8 experts x 7168 bf16 (3.76
 // GB) read and the 0.47 GB of outputs written, the combine takes 716 us (5.9
 // TB/s; a copy runs at 6.4, reads alone at 7.0), 760 us with cached loads and
-// 765 us with cached stores; its gradient, which also writes 3.76 GB, takes
-// 1511 us (5.3 TB/s), 1557 us with cached stores, and does not respond to the
-// rows in flight (8: 1513, 4: 1529, 2: 1531), to pauses between its stores,
-// or to the distance between the two expert buffers: the mix of row-sized
-// reads and writes all over memory bounds it.
+// 765 us with cached stores. Its gradient, which also writes 3.76 GB, takes
+// 1486 us (5.4 TB/s), 46 us more with cached stores. The order of the rows in
+// memory bounds both: with a token's rows in 8 parallel streams the gradient
+// takes 1404 us, with rows at random places 1566; one workgroup per CU is as
+// fast as two, and neither the rows in flight, nor pauses between stores, nor
+// the distance between the two expert buffers makes a difference.
 constexpr int kRowPolicy = kPolicyNT;
 
 // Combine: one-wave workgroups, each one 1 KiB segment of the token's row (two
@@ -41,7 +43,9 @@ constexpr int kSegment = 64 * 16;
 
 // Gradient: a workgroup holds whole rows, because a dot product ends in one
 // number: one 16-byte vector per lane in up to 16 waves, longer rows in
-// several steps (two vectors per lane in half as many waves: 1540 us).
+// several steps (two vectors per lane in half as many waves: 2 % slower).
+// 7 waves per SIMD (at most 72 registers) let two 14-wave workgroups share a
+// CU; room for 8 would spill what the dot products keep (1532 us).
 constexpr int kTokenWaves = 16;
 
 // One lane's slot: the address of its row (0: none) and its weight.
@@ -64,6 +68,13 @@ __device__ __forceinline__ float lane_float(float x, int lane) {
 // The first `bytes` bytes from a wave-uniform address; none from address 0.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(uint64_t at, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, at ? bytes : 0, kRawBufferFormat);
+}
+
+// x of lane ^ N, N below 32.
+template <int N>
+__device__ __forceinline__ float lane_xor(float x) {
+  const int u = static_cast<int>(__float_as_uint(x));
+  return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(u, (N << 10) | 0x1F)));
 }
 
 template <class Args>
@@ -127,35 +138,37 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
       }
     }
   }
-  __builtin_amdgcn_raw_buffer_store_b128(S::narrow(sum), out_rsrc, off, 0, kRowPolicy);
+  __builtin_amdgcn_raw_buffer_store_b128(narrow16<D>(sum), out_rsrc, off, 0, kRowPolicy);
   if (has_tail) *reinterpret_cast<E*>(reinterpret_cast<char*>(out) + tail_off) = S::narrow1(tail);
 }
 
-// Sum of each of Q (a power of two) values over the 64 lanes of a wave, value
-// q left in the lanes with lane % Q == q: halving the number of values while
-// lanes pair up takes Q - 1 + log2(64 / Q) shuffles.
-template <int Q>
-__device__ __forceinline__ float wave_sums(const float* x, int lane) {
-  if constexpr (Q == 1) {
-    return x[0];
-  } else {
-    float y[Q / 2];
-    const bool high = (lane & (Q / 2)) != 0;
+// Sum of each of 8 values over the 64 lanes of a wave, value q in the lanes
+// with lane % 8 == q: halving the number of values while lanes pair up takes
+// 7 + 3 exchanges where summing one value after the other takes 48.
+__device__ __forceinline__ float wave_sums8(const float* x, int lane) {
+  float y[4], z[2];
 #pragma unroll
-    for (int q = 0; q < Q / 2; ++q) {
-      const float keep = high ? x[q + Q / 2] : x[q], give = high ? x[q] : x[q + Q / 2];
-      y[q] = keep + __shfl_xor(give, Q / 2);
-    }
-    return wave_sums<Q / 2>(y, lane);
+  for (int q = 0; q < 4; ++q) {
+    const float keep = lane & 4 ? x[q + 4] : x[q], give = lane & 4 ? x[q] : x[q + 4];
+    y[q] = keep + lane_xor<4>(give);
   }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float keep = lane & 2 ? y[q + 2] : y[q], give = lane & 2 ? y[q] : y[q + 2];
+    z[q] = keep + lane_xor<2>(give);
+  }
+  float s = (lane & 1 ? z[1] : z[0]) + lane_xor<1>(lane & 1 ? z[0] : z[1]);
+  s += lane_xor<8>(s);
+  s += lane_xor<16>(s);
+  return s + __shfl_xor(s, 32);
 }
 
 template <int D, int Q>
-__global__ __launch_bounds__(kTokenWaves * 64) void weighted_backward_kernel(const WeightedBackwardArgs a) {
+__global__ __launch_bounds__(kTokenWaves * 64, 7) void weighted_backward_kernel(const WeightedBackwardArgs a) {
   using S = Storage<D>;
   using E = typename S::elem;
   constexpr int VE = S::kVE;
-  __shared__ float part[kTokenWaves][Q];
+  __shared__ float part[kTokenWaves][8];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int threads = blockDim.x, waves = threads / 64;
   const int i = blockIdx.y;
@@ -179,7 +192,7 @@ __global__ __launch_bounds__(kTokenWaves * 64) void weighted_backward_kernel(con
     }
     const int kn = a.topk - k0 < 64 ? a.topk - k0 : 64;
     for (int k1 = 0; k1 < kn; k1 += Q) {
-      float dot[Q] = {};
+      float dot[8] = {};
       for (int off = tid * 16; off - tid * 16 < whole; off += threads * 16) {
         const u32x4 g4 = __builtin_amdgcn_raw_buffer_load_b128(dy_rsrc, off, 0, kPolicyCached);
         u32x4 row[Q];
@@ -198,7 +211,7 @@ __global__ __launch_bounds__(kTokenWaves * 64) void weighted_backward_kernel(con
             dot[q] = __builtin_fmaf(g[c], f[c], dot[q]);
             d[c] = w * g[c];
           }
-          __builtin_amdgcn_raw_buffer_store_b128(S::narrow(d), row_rsrc(lane_u64(mine.d_at, k1 + q), whole), off, 0,
+          __builtin_amdgcn_raw_buffer_store_b128(narrow16<D>(d), row_rsrc(lane_u64(mine.d_at, k1 + q), whole), off, 0,
                                                  kRowPolicy);
         }
       }
@@ -215,9 +228,7 @@ __global__ __launch_bounds__(kTokenWaves * 64) void weighted_backward_kernel(con
           }
         }
       }
-      float sum = wave_sums<Q>(dot, lane);
-#pragma unroll
-      for (int m = Q; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+      float sum = wave_sums8(dot, lane);
       if (lane < Q) part[wave][lane] = sum;
       __syncthreads();
       if (tid < Q && k1 + tid < kn) {
@@ -246,19 +257,29 @@ hipError_t launch_weighted_backward_q(const WeightedBackwardArgs& a, hipStream_t
   return launch(weighted_backward_kernel<D, Q>, grid, block, a, stream);
 }
 
-// Q: rows in flight, the chosen experts of a token where they are few.
+// Rows in flight: the even number up to 8 that wastes the fewest places on a
+// token's topk rows (7 and 8 take 8, 6 takes 6, 10 takes 6 twice).
+template <class F>
+hipError_t by_rows(int topk, F&& run) {
+  using std::integral_constant;
+  int best = 8;
+  for (int q : {6, 4, 2})
+    if ((topk + q - 1) / q * q < (topk + best - 1) / best * best) best = q;
+  if (topk > 8 && best < 6) best = 6;               // long lists: fewer steps rather than fewer idle places
+  if (best == 2) return run(integral_constant<int, 2>{});
+  if (best == 4) return run(integral_constant<int, 4>{});
+  if (best == 6) return run(integral_constant<int, 6>{});
+  return run(integral_constant<int, 8>{});
+}
+
 template <int D>
 hipError_t launch_weighted_dt(const WeightedArgs& a, hipStream_t stream) {
-  if (a.topk <= 2) return launch_weighted_q<D, 2>(a, stream);
-  if (a.topk <= 4) return launch_weighted_q<D, 4>(a, stream);
-  return launch_weighted_q<D, 8>(a, stream);
+  return by_rows(a.topk, [&](auto q) { return launch_weighted_q<D, decltype(q)::value>(a, stream); });
 }
 
 template <int D>
 hipError_t launch_weighted_backward_dt(const WeightedBackwardArgs& a, hipStream_t stream) {
-  if (a.topk <= 2) return launch_weighted_backward_q<D, 2>(a, stream);
-  if (a.topk <= 4) return launch_weighted_backward_q<D, 4>(a, stream);
-  return launch_weighted_backward_q<D, 8>(a, stream);
+  return by_rows(a.topk, [&](auto q) { return launch_weighted_backward_q<D, decltype(q)::value>(a, stream); });
 }
 
 }  // namespace

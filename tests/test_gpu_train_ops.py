@@ -66,6 +66,8 @@ ROUTES = [(1, 1, 1, 1, "f32", False), (1, 1, 256, 8, "f32", False), (2, 5, 7, 7,
           (3, 17, 64, 64, "f32", True), (5, 9, 65, 3, "bf16", True), (2, 33, 128, 2, "f32", True),
           (8, 6, 256, 8, "bf16", False), (1, 40, 255, 10, "f32", True), (2, 11, 300, 8, "f32", True),
           (1, 7, 512, 6, "bf16", False), (1, 9, 1024, 8, "f32", True), (1, 5, 1000, 64, "bf16", True),
+          (2, 9, 480, 7, "bf16", True), (1, 7, 770, 8, "f32", True),
+          (1, 6, 100, 33, "f32", True), (1, 6, 250, 17, "bf16", False), (1, 5, 600, 40, "f32", True),
           (40, 2, 24, 2, "f32", True), (128, 1, 16, 1, "bf16", False), (1, 1, 130, 5, "f32", False)]
 
 
