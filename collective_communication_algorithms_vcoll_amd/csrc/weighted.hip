@@ -9,7 +9,7 @@
 // k in slot order); one rounding per stored element. A slot outside the
 // expert buffers contributes nothing.
 //
-// The rows of up to 64 slots are looked up at once, one per lane, and each
+// The rows of some 64 slots are looked up at once, one per lane, and each
 // then becomes a wave-uniform buffer resource. Looking them up one after the
 // other would put 2 K dependent scalar loads before the first row load. A
 // slot without a row gets a resource of no bytes: its loads return zeros and
@@ -90,6 +90,7 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
   using S = Storage<D>;
   using E = typename S::elem;
   constexpr int VE = S::kVE;
+  constexpr int kLookup = 64 / Q * Q;                // slots looked up at once: whole steps of Q lanes
   const int lane = threadIdx.x;
   const int i = blockIdx.y;
   const int seg = static_cast<int>(blockIdx.x % a.segments);
@@ -104,9 +105,9 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
   const int off = seg * kSegment + lane * 16;
   const int tail_off = whole + lane * static_cast<int>(sizeof(E));
   const bool has_tail = seg == 0 && tail_off < row_bytes;
-  for (int k0 = 0; k0 < a.topk; k0 += 64) {
+  for (int k0 = 0; k0 < a.topk; k0 += kLookup) {
     Row mine = {0, 0, 0.0f};
-    if (k0 + lane < a.topk) {
+    if (lane < kLookup && k0 + lane < a.topk) {
       int j;
       const int64_t r = row_of(a, slot, k0 + lane, j);
       if (r >= 0) {
@@ -114,7 +115,7 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
         mine.weight = a.weights[i] ? a.weights[i][t * a.topk + k0 + lane] : 1.0f;
       }
     }
-    const int kn = a.topk - k0 < 64 ? a.topk - k0 : 64;
+    const int kn = a.topk - k0 < kLookup ? a.topk - k0 : kLookup;
     for (int k1 = 0; k1 < kn; k1 += Q) {
       u32x4 row[Q];
 #pragma unroll
@@ -168,6 +169,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 7) void weighted_backward_kernel(
   using S = Storage<D>;
   using E = typename S::elem;
   constexpr int VE = S::kVE;
+  constexpr int kLookup = 64 / Q * Q;
   __shared__ float part[kTokenWaves][8];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int threads = blockDim.x, waves = threads / 64;
@@ -179,9 +181,9 @@ __global__ __launch_bounds__(kTokenWaves * 64, 7) void weighted_backward_kernel(
   const int whole = row_bytes / 16 * 16;
   const auto dy_rsrc = row_rsrc(reinterpret_cast<uint64_t>(dy), whole);
   const int tail_off = whole + tid * static_cast<int>(sizeof(E));
-  for (int k0 = 0; k0 < a.topk; k0 += 64) {
+  for (int k0 = 0; k0 < a.topk; k0 += kLookup) {
     Row mine = {0, 0, 0.0f};
-    if (k0 + lane < a.topk) {
+    if (lane < kLookup && k0 + lane < a.topk) {
       int j;
       const int64_t r = row_of(a, slot, k0 + lane, j);
       if (r >= 0) {
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 7) void weighted_backward_kernel(
         mine.weight = a.weights[i][t * a.topk + k0 + lane];
       }
     }
-    const int kn = a.topk - k0 < 64 ? a.topk - k0 : 64;
+    const int kn = a.topk - k0 < kLookup ? a.topk - k0 : kLookup;
     for (int k1 = 0; k1 < kn; k1 += Q) {
       float dot[8] = {};
       for (int off = tid * 16; off - tid * 16 < whole; off += threads * 16) {

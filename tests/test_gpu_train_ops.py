@@ -299,7 +299,8 @@ def put_ids(x):
 
 COMBINES = [(1, 1, 1, 1, 1, "f32"), (1, 1, 8, 7168, 8, "bf16"), (2, 5, 2, 16, 3, "bf16"), (3, 9, 3, 1001, 2, "f32"),
             (3, 9, 3, 1001, 2, "bf16"), (8, 4, 8, 512, 32, "bf16"), (2, 3, 9, 260, 8, "f32"), (1, 2, 17, 4096, 20, "bf16"),
-            (1, 3, 4, 9000, 6, "bf16"), (4, 6, 2, 2056, 2, "f32"), (40, 2, 2, 64, 1, "f32"), (2, 4, 33, 40, 20, "bf16"),
+            (1, 3, 4, 9000, 6, "bf16"), (4, 6, 2, 2056, 2, "f32"), (40, 2, 2, 64, 1, "f32"), (2, 4, 33, 40, 20, "bf16"), (1, 3, 70, 24, 80, "f32"), (1, 2, 62, 16, 64, "bf16"),
+            (1, 2, 130, 9, 132, "f32"),
             (2, 7, 5, 8, 4, "bf16"), (2, 7, 1, 3, 4, "bf16")]
 
 
