@@ -37,8 +37,12 @@ using namespace dev;
 // the distance between the two expert buffers makes a difference.
 constexpr int kRowPolicy = kPolicyNT;
 
-// Combine: one-wave workgroups, each one 1 KiB segment of the token's row (two
-// vectors per lane 740 us, four-wave workgroups 765, seven-wave 727).
+// Combine: one-wave workgroups, each one segment of V KiB of the token's row
+// (8 rows: two vectors per lane 740 us, four-wave workgroups 765, seven-wave
+// 727). With two rows per token a wave takes up to 4 KiB of each, so that it
+// has 8 KiB to wait for after its look-ups too: 8 x 4096 tokens of 2 x 2048
+// bf16 66 us (95 % of a copy's rate), 79 in segments of 1 KiB. With four rows
+// 1 KiB is enough (2 KiB: 4 x 2048 float32 215 -> 227 us).
 constexpr int kSegment = 64 * 16;
 
 // Gradient: a workgroup holds whole rows, because a dot product ends in one
@@ -85,7 +89,7 @@ __device__ __forceinline__ int64_t row_of(const Args& a, const int32_t* slot, in
   return r;
 }
 
-template <int D, int Q>
+template <int D, int Q, int V>
 __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
   using S = Storage<D>;
   using E = typename S::elem;
@@ -100,9 +104,9 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
   const int whole = row_bytes / 16 * 16;
   E* out = static_cast<E*>(a.out[i]) + t * a.hidden;
   const auto out_rsrc = row_rsrc(reinterpret_cast<uint64_t>(out), whole);
-  float sum[VE] = {};
+  float sum[V][VE] = {};
   float tail = 0.0f;                                 // element whole / sizeof(E) + lane of the row
-  const int off = seg * kSegment + lane * 16;
+  const int off = seg * V * kSegment + lane * 16;
   const int tail_off = whole + lane * static_cast<int>(sizeof(E));
   const bool has_tail = seg == 0 && tail_off < row_bytes;
   for (int k0 = 0; k0 < a.topk; k0 += kLookup) {
@@ -117,17 +121,24 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
     }
     const int kn = a.topk - k0 < kLookup ? a.topk - k0 : kLookup;
     for (int k1 = 0; k1 < kn; k1 += Q) {
-      u32x4 row[Q];
+      u32x4 row[Q][V];
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        row[q] = __builtin_amdgcn_raw_buffer_load_b128(row_rsrc(lane_u64(mine.at, k1 + q), whole), off, 0, kRowPolicy);
+      for (int q = 0; q < Q; ++q) {
+        const auto rsrc = row_rsrc(lane_u64(mine.at, k1 + q), whole);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          row[q][v] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + v * kSegment, 0, kRowPolicy);
+      }
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const float w = lane_float(mine.weight, k1 + q);
-        float f[VE];
-        S::widen(row[q], f);
 #pragma unroll
-        for (int c = 0; c < VE; ++c) sum[c] = __builtin_fmaf(w, f[c], sum[c]);
+        for (int v = 0; v < V; ++v) {
+          float f[VE];
+          S::widen(row[q][v], f);
+#pragma unroll
+          for (int c = 0; c < VE; ++c) sum[v][c] = __builtin_fmaf(w, f[c], sum[v][c]);
+        }
       }
     }
     if (whole != row_bytes) {
@@ -139,7 +150,9 @@ __global__ __launch_bounds__(64) void weighted_kernel(const WeightedArgs a) {
       }
     }
   }
-  __builtin_amdgcn_raw_buffer_store_b128(narrow16<D>(sum), out_rsrc, off, 0, kRowPolicy);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    __builtin_amdgcn_raw_buffer_store_b128(narrow16<D>(sum[v]), out_rsrc, off + v * kSegment, 0, kRowPolicy);
   if (has_tail) *reinterpret_cast<E*>(reinterpret_cast<char*>(out) + tail_off) = S::narrow1(tail);
 }
 
@@ -243,12 +256,22 @@ __global__ __launch_bounds__(kTokenWaves * 64, 7) void weighted_backward_kernel(
   }
 }
 
-template <int D, int Q>
-hipError_t launch_weighted_q(WeightedArgs a, hipStream_t stream) {
-  const int64_t row_bytes = a.hidden * sizeof(typename Storage<D>::elem);
-  a.segments = static_cast<int32_t>(row_bytes > kSegment ? (row_bytes / 16 * 16 + kSegment - 1) / kSegment : 1);
+template <int D, int Q, int V>
+hipError_t launch_weighted_v(WeightedArgs a, hipStream_t stream) {
+  const int64_t whole = a.hidden * sizeof(typename Storage<D>::elem) / 16 * 16;
+  a.segments = static_cast<int32_t>(std::max<int64_t>(1, (whole + V * kSegment - 1) / (V * kSegment)));
   const dim3 grid(static_cast<unsigned>(a.tokens * a.segments), a.ranks);
-  return launch(weighted_kernel<D, Q>, grid, 64, a, stream);
+  return launch(weighted_kernel<D, Q, V>, grid, 64, a, stream);
+}
+
+template <int D, int Q>
+hipError_t launch_weighted_q(const WeightedArgs& a, hipStream_t stream) {
+  const int64_t row_bytes = a.hidden * sizeof(typename Storage<D>::elem);
+  if constexpr (Q == 2) {
+    if (row_bytes > 2 * kSegment) return launch_weighted_v<D, Q, 4>(a, stream);
+    if (row_bytes > kSegment) return launch_weighted_v<D, Q, 2>(a, stream);
+  }
+  return launch_weighted_v<D, Q, 1>(a, stream);
 }
 
 template <int D, int Q>
