@@ -17,6 +17,7 @@ from __future__ import annotations
 import bisect
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 import numpy as np
@@ -116,7 +117,7 @@ def _lib():
         lib.vcoll_moe_expand_slots.restype = I
         lib.vcoll_moe_dedup_slots.argtypes = [I, I64, I, P(I64), P(ctypes.c_int32), P(ctypes.c_int32)]
         lib.vcoll_moe_dedup_slots.restype = I
-        lib.vcoll_moe_dispatch.argtypes = [I, I64, I, I64, I, I, P(VP), P(VP), P(VP), P(I64), VP]
+        lib.vcoll_moe_dispatch.argtypes = [I, I64, I, I64, I, I, VP, VP, VP, VP, VP]
         lib.vcoll_moe_dispatch.restype = I
         lib.vcoll_moe_combine.argtypes = [I, I64, I, I64, I, P(VP), P(I64), P(VP), P(VP), VP]
         lib.vcoll_moe_combine.restype = I
@@ -773,22 +774,24 @@ def vcoll_moe_dispatch(tokens, slots, recv_rows, topk: int, fp8: bool = False, r
             recv = [torch.empty((rr[j], H + H // 32), dtype=torch.uint8, device=dev) for j in range(p)]
         else:
             recv = [torch.empty((rr[j], H), dtype=dt, device=dev) for j in range(p)]
-    r = list(recv)
+    r, s, rr = list(recv)[:p], list(slots)[:p], rr[:p]
+    if not len(r) == len(s) == len(rr) == p:
+        raise ValueError(f"vcoll_moe_dispatch: need {p} receive buffers, row counts and slot tables")
     orb = H + H // 32 if fp8 else H * t[0].element_size()
     for j in range(p):
         if not r[j].is_contiguous() or r[j].nbytes < rr[j] * orb:
             raise ValueError(f"vcoll_moe_dispatch: recv[{j}] holds fewer than {rr[j]} rows")
         if r[j].device != dev:
             raise ValueError(f"vcoll_moe_dispatch: recv[{j}] is on {r[j].device}, the token tables on {dev}")
-    s = list(slots)
     for x in s:
         if x.dtype != torch.int32 or x.device != dev or x.numel() < 2 * T * topk:
             raise ValueError("vcoll_moe_dispatch: slots must be int32 GPU tensors of T*topk pairs")
     _on_current_gpu(t[0])                         # every buffer shares its device
     _apart(t, r, "vcoll_moe_dispatch")
-    table = lambda ts: (ctypes.c_void_p * len(ts))(*[x.data_ptr() or None for x in ts])            # noqa: E731
+    pack = struct.Struct(f"{p}q").pack
+    table = lambda ts: pack(*[x.data_ptr() for x in ts])                                         # noqa: E731
     _check(_lib().vcoll_moe_dispatch(p, T, topk, H, _dtype_code(t[0]), int(bool(fp8)), table(t), table(s), table(r),
-                                     (ctypes.c_int64 * p)(*rr), _stream(t[0])), "vcoll_moe_dispatch")
+                                     pack(*rr), _stream(t[0])), "vcoll_moe_dispatch")
     return recv
 
 

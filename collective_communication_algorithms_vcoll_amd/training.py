@@ -12,6 +12,8 @@ sequence.
 from __future__ import annotations
 
 import ctypes
+import struct
+from functools import lru_cache
 
 import torch
 
@@ -33,16 +35,16 @@ class _AdamwHyper(ctypes.Structure):
 
 
 def _declare(lib) -> None:
-    P, I, I64, VP = ctypes.POINTER, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
-    lib.vcoll_moe_route.argtypes = [I, I64, I, I, I, I, P(VP), P(VP), P(VP), VP]
-    lib.vcoll_moe_route_backward.argtypes = [I, I64, I, I, I, I, P(VP), P(VP), P(VP), P(VP), P(VP), VP]
-    lib.vcoll_moe_sort.argtypes = [I, I64, I, I, P(VP), P(VP), VP, VP, I64, VP]
+    # tables of addresses and row counts travel as packed bytes: V
+    P, I, I64, V = ctypes.POINTER, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+    lib.vcoll_moe_route.argtypes = [I, I64, I, I, I, I, V, V, V, V]
+    lib.vcoll_moe_route_backward.argtypes = [I, I64, I, I, I, I, V, V, V, V, V, V]
+    lib.vcoll_moe_sort.argtypes = [I, I64, I, I, V, V, V, V, I64, V]
     lib.vcoll_moe_sort_workspace.argtypes = [I, I64, I, I, P(I64)]
-    lib.vcoll_moe_combine_weighted.argtypes = [I, I64, I, I64, I, P(VP), P(I64), P(VP), P(VP), P(VP), VP]
-    lib.vcoll_moe_combine_weighted_backward.argtypes = [I, I64, I, I64, I, P(VP), P(VP), P(I64), P(VP), P(VP), P(VP),
-                                                        P(VP), VP]
-    lib.vcoll_adamw.argtypes = [I, P(_AdamwTensor), I, I, I, P(_AdamwHyper), VP]
-    lib.vcoll_adamw_unpack.argtypes = [I64, VP, VP, VP, VP, VP, VP, VP]
+    lib.vcoll_moe_combine_weighted.argtypes = [I, I64, I, I64, I, V, V, V, V, V, V]
+    lib.vcoll_moe_combine_weighted_backward.argtypes = [I, I64, I, I64, I, V, V, V, V, V, V, V, V]
+    lib.vcoll_adamw.argtypes = [I, P(_AdamwTensor), I, I, I, P(_AdamwHyper), V]
+    lib.vcoll_adamw_unpack.argtypes = [I64, V, V, V, V, V, V, V]
     for name in ("route", "route_backward", "sort", "sort_workspace", "combine_weighted", "combine_weighted_backward"):
         getattr(lib, "vcoll_moe_" + name).restype = I
     lib.vcoll_adamw.restype = I
@@ -74,15 +76,19 @@ def _first(x, what: str, name: str, dims: int):
     return p, shape, t
 
 
-def _addresses(x, p: int):
+@lru_cache(maxsize=None)
+def _packer(p: int):
+    """Packs p 64-bit values: a table that a C entry point reads during the call."""
+    return struct.Struct(f"{p}q").pack
+
+
+def _addresses(x, p: int) -> bytes:
     """The addresses of the p rank buffers of a checked argument."""
     if isinstance(x, torch.Tensor):
-        size = x.nbytes
-        if not size:
-            return (ctypes.c_void_p * p)()
         base = x.data_ptr()
-        return (ctypes.c_void_p * p)(*range(base, base + size, size // p))
-    return (ctypes.c_void_p * p)(*[t.data_ptr() or None for t in x])
+        step = x.nbytes // p
+        return _packer(p)(*range(base, base + p * step, step)) if step else bytes(8 * p)
+    return _packer(p)(*[t.data_ptr() for t in x])
 
 
 def _table(x, p: int, shape: tuple, dtype, dev, what: str, name: str):
@@ -255,7 +261,7 @@ def vcoll_moe_combine_weighted(expert_out, slots, weights, tokens: int, topk: in
     out, o, ot = _result(out, slots, p, (T, H), dt, dev, what, "out")
     if ot:
         _apart(expert_out + st + wt, ot, what)
-    _check(_lib().vcoll_moe_combine_weighted(p, T, K, H, code, e, (ctypes.c_int64 * p)(*rows), s, w, o, _stream(t)),
+    _check(_lib().vcoll_moe_combine_weighted(p, T, K, H, code, e, _packer(p)(*rows), s, w, o, _stream(t)),
            what)
     return out
 
@@ -288,7 +294,7 @@ def vcoll_moe_combine_weighted_backward(d_out, expert_out, slots, weights, topk:
     d_weights, dw, dwt = _result(d_weights, d_out, p, (T, K), torch.float32, dev, what, "d_weights")
     if written or dwt:
         _apart(gt + st + wt + expert_out, written + dwt, what)
-    _check(_lib().vcoll_moe_combine_weighted_backward(p, T, K, H, code, g, e, (ctypes.c_int64 * p)(*rows), s, w, de, dw,
+    _check(_lib().vcoll_moe_combine_weighted_backward(p, T, K, H, code, g, e, _packer(p)(*rows), s, w, de, dw,
                                                       _stream(t)), what)
     return d_expert_out, d_weights
 
