@@ -107,17 +107,13 @@ def _table(x, p: int, shape: tuple, dtype, dev, what: str, name: str):
     return _addresses(x, p), list(x)
 
 
-def _new(like, p: int, shape: tuple, dtype, dev):
-    """New rank buffers in the form of `like`."""
-    if isinstance(like, torch.Tensor):
-        return torch.empty((p, *shape), dtype=dtype, device=dev)
-    return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(p)]
-
-
 def _result(x, like, p: int, shape: tuple, dtype, dev, what: str, name: str):
     """(rank buffers to write, their addresses, the given tensors): `x` after the checks, or new ones."""
     if x is None:
-        x = _new(like, p, shape, dtype, dev)
+        if isinstance(like, torch.Tensor):
+            x = torch.empty((p, *shape), dtype=dtype, device=dev)
+        else:
+            x = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(p)]
         return x, _addresses(x, p), []
     return (x, *_table(x, p, shape, dtype, dev, what, name))
 
@@ -232,9 +228,11 @@ def _expert_rows(expert, p: int, hidden: int, dtype, dev, what: str, name: str):
     if len(expert) != p:
         raise ValueError(f"{what}: {name} must hold {p} rank buffers, got {len(expert)}")
     rows = []
+    at = dev.index if dev.index is not None else -1          # get_device() of a CPU tensor
     for t in expert:
         shape = t.shape
-        if len(shape) != 2 or shape[1] != hidden or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        if len(shape) != 2 or shape[1] != hidden or t.dtype is not dtype or t.get_device() != at or \
+                not t.is_contiguous():
             raise ValueError(f"{what}: every {name} must be a contiguous {dtype} tensor [rows, {hidden}] on {dev}, "
                              f"got {t.dtype} {tuple(shape)} on {t.device}")
         rows.append(shape[0])
