@@ -27,8 +27,11 @@ bool valid_router(int p, int64_t tokens, int experts, int topk, int dtype) {
          pairs_fit(tokens, topk) && fits(tokens, static_cast<int64_t>(experts) * 4);
 }
 
-// x workgroups of up to 1024 threads each stay within 2^32 threads of a grid dimension
-bool grid_fits(int64_t groups) { return groups <= (int64_t(UINT32_MAX) >> 10); }
+// `groups` workgroups of kBlock threads stay within the 2^32 threads of a grid dimension
+bool grid_fits(int64_t groups) { return groups <= int64_t(UINT32_MAX) / kBlock; }
+
+// the router's: 4 tokens per workgroup where a wave has one token
+bool tokens_fit(int64_t tokens) { return grid_fits((tokens + 3) / 4); }
 
 // Calls run(first rank, ranks) for groups of at most kTokenRanks ranks.
 template <class F>
@@ -77,9 +80,9 @@ vcoll_status check_rows(int p, int64_t tokens, int topk, int64_t hidden, int dty
   if (!fits(tokens, rb)) return VCOLL_ERR_INVALID_ARG;
   for (int j = 0; j < p; ++j)
     if (expert_rows[j] < 0 || expert_rows[j] > INT32_MAX || !fits(expert_rows[j], rb)) return VCOLL_ERR_INVALID_ARG;
-  // one workgroup of up to 1024 threads per token, or of 64 threads per KiB of its row
-  const bool fit = grid_fits(tokens) && tokens * std::max<int64_t>(1, (rb + 1023) / 1024) <= (int64_t(UINT32_MAX) >> 6);
-  return fit ? VCOLL_OK : VCOLL_ERR_UNSUPPORTED;
+  // at most one wave per KiB of a token's row
+  const int64_t waves = tokens * std::max<int64_t>(1, (rb + 1023) / 1024);
+  return waves <= int64_t(UINT32_MAX) / 64 ? VCOLL_OK : VCOLL_ERR_UNSUPPORTED;
 }
 
 bool valid_hyper(const vcoll_adamw_hyper* h) {
@@ -95,7 +98,7 @@ extern "C" {
 vcoll_status vcoll_moe_route(int p, int64_t tokens, int experts, int topk, vcoll_dtype dtype, int normalise,
                              const void* const* logits, int32_t* const* ids, float* const* weights, void* stream) {
   if (!valid_router(p, tokens, experts, topk, dtype)) return VCOLL_ERR_INVALID_ARG;
-  if (experts > kMaxExperts || topk > kMaxTopk || !grid_fits(tokens)) return VCOLL_ERR_UNSUPPORTED;
+  if (experts > kMaxExperts || topk > kMaxTopk || !tokens_fit(tokens)) return VCOLL_ERR_UNSUPPORTED;
   if (tokens == 0) return VCOLL_OK;
   if (!all_set(p, logits) || !all_given(p, ids) || !all_given(p, weights)) return VCOLL_ERR_INVALID_ARG;
   for (int i = 0; i < p; ++i)
@@ -122,7 +125,7 @@ vcoll_status vcoll_moe_route_backward(int p, int64_t tokens, int experts, int to
                                       const float* const* weights, const float* const* d_weights,
                                       void* const* d_logits, void* stream) {
   if (!valid_router(p, tokens, experts, topk, dtype)) return VCOLL_ERR_INVALID_ARG;
-  if (experts > kMaxExperts || topk > kMaxTopk || !grid_fits(tokens)) return VCOLL_ERR_UNSUPPORTED;
+  if (experts > kMaxExperts || topk > kMaxTopk || !tokens_fit(tokens)) return VCOLL_ERR_UNSUPPORTED;
   if (tokens == 0) return VCOLL_OK;
   if ((!normalise && !all_set(p, logits)) || !all_given(p, ids) || !all_given(p, weights) || !all_given(p, d_weights) ||
       !all_given(p, d_logits))

@@ -132,11 +132,12 @@ def mix(x: np.ndarray) -> np.ndarray:
     return x ^ (x >> np.uint64(16))
 
 
-def rounding_bits(n: int, seed: int, step: int, tensor: int) -> np.ndarray:
-    """The 32 random bits of elements 0..n-1 of the call's tensor number `tensor`."""
+def rounding_bits(n: int, seed: int, step: int, tensor: int, start: int = 0) -> np.ndarray:
+    """The 32 random bits of n elements, from `start` on, of the call's tensor number `tensor`."""
     first = mix(seed + int(mix(step)))
     key = mix(int(first) + 0x9E3779B9 * tensor & 0xFFFFFFFF)
-    return mix(np.arange(n, dtype=np.uint64) + np.uint64(key))
+    index = np.arange(start, start + n, dtype=np.uint64)
+    return mix((index & np.uint64(0xFFFFFFFF)) + key + mix(index >> np.uint64(32)))
 
 
 class Format:

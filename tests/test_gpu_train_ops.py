@@ -153,6 +153,24 @@ def test_route_values_at_the_edges(vc):
         assert np.isfinite(dz[0, 2:]).all() and (dz[0, 4, :68] == 0).all()
 
 
+def test_route_beyond_2_31_logits(vc):
+    """The last tokens of a table of more than 2^31 logits."""
+    import torch
+    T, E = 9_000_000, 250
+    z = torch.zeros((1, T, E), device="cuda", dtype=torch.bfloat16)
+    tail = torch.randn((40, E), device="cuda").to(torch.bfloat16)
+    z[0, -40:] = tail
+    ids, w = vc.vcoll_moe_route(z, 3)
+    want_ids, want_w = vc.vcoll_moe_route(tail[None].contiguous(), 3)
+    assert torch.equal(ids[0, -40:], want_ids[0]) and torch.equal(w[0, -40:], want_w[0])
+    assert bool((ids[0, :-40] == torch.arange(3, device="cuda")).all())
+    dw = torch.randn((1, T, 3), device="cuda")
+    dz = vc.vcoll_moe_route_backward(z, ids, w, dw, normalise=False)
+    want = vc.vcoll_moe_route_backward(tail[None].contiguous(), want_ids, want_w, dw[:, -40:].contiguous(),
+                                       normalise=False)
+    assert torch.equal(dz[0, -40:], want[0])
+
+
 def test_route_list_and_given_outputs(vc):
     import torch
     z, _ = logits(3, 5, 20, "f32", 1, True)
@@ -532,6 +550,28 @@ def test_adamw_many_tensors(vc):
                 m, v = train.encode_m(m, b)[0], train.encode_v(v, b)[0]
             same_bits(dev["exp_avg"][k], m, f"tensor {k}")
             same_bits(dev["exp_avg_sq"][k], v, f"tensor {k}")
+
+
+def test_adamw_beyond_2_32_elements(vc):
+    """The last 1500 elements of a tensor of 2^32 + 1500 with 8-bit states: offsets and random bits past 32 bits."""
+    import torch
+    n, m = 2 ** 32 + 1500, 1500
+    x = torch.zeros(n, device="cuda")
+    g = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
+    state = vc.adamw_state([x], 8)
+    rng = np.random.default_rng(8)
+    xs = (rng.normal(size=m) * 0.1).astype(np.float32)
+    x[-m:].copy_(torch.from_numpy(xs))
+    g[-m:].copy_(torch.from_numpy((rng.normal(size=m) * 1e-3).astype(np.float32)))
+    gs = g[-m:].float().cpu().numpy()
+    vc.vcoll_adamw([x], [g], **state, step=1, seed=4, **HYPER)
+    z = np.zeros(m, np.float32)
+    want, wm, wv = train.adamw(xs, gs, z, z, step=1, **HYPER)
+    b = train.rounding_bits(m, 4, 1, 0, 2 ** 32)
+    same_bits(x[-m:], want, "parameters")
+    same_bits(state["exp_avg"][0][-m:], train.encode_m(wm, b)[0], "exp_avg")
+    same_bits(state["exp_avg_sq"][0][-m:], train.encode_v(wv, b)[0], "exp_avg_sq")
+    assert not bool(x[:-m].any()) and not bool(state["exp_avg"][0][:-m].any())
 
 
 def test_adamw_from_zero_states(vc):

@@ -175,7 +175,7 @@ def call_route(p=1, tokens=4, experts=8, topk=2, dtype=0, logits=(ADDR,), ids=(A
     (dict(p=0), INVALID), (dict(p=129), INVALID), (dict(tokens=-1), INVALID), (dict(tokens=2 ** 48 + 1), INVALID),
     (dict(experts=0), INVALID), (dict(topk=0), INVALID), (dict(topk=9), INVALID), (dict(dtype=2), INVALID),
     (dict(dtype=7), INVALID), (dict(tokens=2 ** 31), INVALID), (dict(experts=1025), UNSUPPORTED),
-    (dict(experts=100, topk=65), UNSUPPORTED), (dict(tokens=2 ** 24), UNSUPPORTED), (dict(logits=(None,)), INVALID),
+    (dict(experts=100, topk=65), UNSUPPORTED), (dict(tokens=2 ** 27), UNSUPPORTED), (dict(logits=(None,)), INVALID),
     (dict(ids=(None,)), INVALID), (dict(weights=(None,)), INVALID), (dict(logits=(ADDR + 2,)), INVALID),
     (dict(dtype=1, logits=(ADDR + 1,)), INVALID), (dict(ids=(ADDR + 2,)), INVALID), (dict(weights=(ADDR + 1,)), INVALID),
 ])
@@ -241,7 +241,7 @@ def call_combine(p=1, tokens=4, topk=2, hidden=16, dtype=0, e=(ADDR,), n=(8,), s
 @pytest.mark.parametrize("change,status", [
     (dict(p=0), INVALID), (dict(tokens=-1), INVALID), (dict(topk=0), INVALID), (dict(hidden=-1), INVALID),
     (dict(hidden=2 ** 31), INVALID), (dict(dtype=2), INVALID), (dict(n=(-1,)), INVALID), (dict(n=(2 ** 31,)), INVALID),
-    (dict(tokens=2 ** 30), INVALID), (dict(tokens=2 ** 24), UNSUPPORTED), (dict(e=(None,)), INVALID),
+    (dict(tokens=2 ** 30), INVALID), (dict(tokens=2 ** 27), UNSUPPORTED), (dict(e=(None,)), INVALID),
     (dict(slots=(None,)), INVALID), (dict(weights=(None,)), INVALID), (dict(out=(None,)), INVALID),
     (dict(e=(ADDR + 2,)), INVALID), (dict(out=(ADDR + 1,), dtype=1), INVALID), (dict(weights=(ADDR + 2,)), INVALID),
     (dict(slots=(ADDR + 2,)), INVALID),
@@ -262,7 +262,7 @@ def call_combine_backward(p=1, tokens=4, topk=2, hidden=16, dtype=0, dy=(ADDR,),
 
 @pytest.mark.parametrize("change,status", [
     (dict(p=0), INVALID), (dict(tokens=-1), INVALID), (dict(topk=0), INVALID), (dict(hidden=0), INVALID),
-    (dict(dtype=2), INVALID), (dict(n=(-1,)), INVALID), (dict(tokens=2 ** 24), UNSUPPORTED), (dict(dy=(None,)), INVALID),
+    (dict(dtype=2), INVALID), (dict(n=(-1,)), INVALID), (dict(tokens=2 ** 27), UNSUPPORTED), (dict(dy=(None,)), INVALID),
     (dict(e=(None,)), INVALID), (dict(slots=(None,)), INVALID), (dict(weights=(None,)), INVALID),
     (dict(de=(None,)), INVALID), (dict(dw=(None,)), INVALID), (dict(dy=(ADDR + 2,)), INVALID),
     (dict(e=(ADDR + 2,)), INVALID), (dict(de=(ADDR + 2,)), INVALID), (dict(dw=(ADDR + 2,)), INVALID),
