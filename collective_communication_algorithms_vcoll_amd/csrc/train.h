@@ -16,8 +16,8 @@ namespace vcoll {
 // 4 KiB); more ranks take further launches.
 constexpr int kTokenRanks = 32;
 
-constexpr int kMaxExperts = 1024;    // experts of one router or sort: one thread, or 16 per lane, each
-constexpr int kMaxTopk = 64;         // chosen experts per token: one lane each
+constexpr int kMaxExperts = 1024;    // of one router or sort: a thread of the sort each, up to 64 per lane of the router
+constexpr int kMaxTopk = 64;         // chosen experts per token: up to 4 per lane of the router
 
 // Grid: x = token tiles, y = rank.
 struct RouteArgs {
@@ -28,6 +28,7 @@ struct RouteArgs {
   int32_t experts, topk, normalise;
   int32_t ranks;                     // ranks of this launch
 };
+static_assert(sizeof(RouteArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
 struct RouteBackwardArgs {
   const void* logits[kTokenRanks];
@@ -39,6 +40,7 @@ struct RouteBackwardArgs {
   int32_t experts, topk, normalise;
   int32_t ranks;
 };
+static_assert(sizeof(RouteBackwardArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
 // Pairs in (rank, token, slot) order are cut into `blocks` tiles of `tile`.
 struct SortArgs {

@@ -602,8 +602,8 @@ vcoll_status vcoll_moe_sort_workspace(int p, int64_t tokens, int topk, int exper
  * its experts' outputs). For every rank i and token t < tokens
  *   out[i][t] = sum_k weights[i][t*topk + k] * expert_out[j][r],
  *   (j, r) = slots[i][t*topk + k],
- * rows of hidden elements of dtype, summed in float32 in slot order and
- * rounded once. weights NULL: all ones, which is the gradient of
+ * rows of hidden elements of dtype, summed in float32 in slot order (fused
+ * multiply-adds) and rounded once. weights NULL: all ones, which is the gradient of
  * vcoll_moe_dispatch. A slot outside [0, p) x [0, expert_rows[j]) contributes
  * nothing (whatever its weight); a token without slots gets zeros. Buffers
  * must not overlap and need only be aligned to their elements. hidden <= 2^28.
@@ -674,7 +674,8 @@ typedef struct vcoll_adamw_hyper {
  * key = mix(mix(seed + mix(step)) + 0x9E3779B9 * tensor) of the tensor's
  * position in the call and mix(x): x ^= x >> 16, x *= 0x9E3779B1, x ^= x >> 15,
  * x *= 0x85157AF5, x ^= x >> 16, modulo 2^32. The update uses the m and v of
- * this step before their rounding. Zeros are a valid initial state. No
+ * this step before their rounding. Zeros are a valid initial state (with eps
+ * 0 an element without any gradient so far becomes NaN, 0/0). No
  * buffer may overlap another, and beta1, beta2 are in [0, 1). One launch per
  * 48 tensors; a captured launch keeps its step.
  */
