@@ -153,6 +153,53 @@ def test_route_values_at_the_edges(vc):
         assert np.isfinite(dz[0, 2:]).all() and (dz[0, 4, :68] == 0).all()
 
 
+def shifted(x, by=1):
+    """A copy of x that starts `by` elements off its allocation's alignment."""
+    import torch
+    flat = torch.empty(x.numel() + by, dtype=x.dtype, device="cuda")
+    y = flat[by:].view(x.shape)
+    y.copy_(x)
+    return y
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+def test_route_of_unaligned_views(vc, name):
+    import torch
+    for E, K in ((64, 2), (256, 8), (256, 12), (1024, 8), (40, 3)):
+        z, _ = logits(2, 19, E, name, E + K, True)
+        dw = put(np.random.default_rng(E).normal(size=(2, 19, K)))
+        for normalise in (True, False):
+            ids, w = vc.vcoll_moe_route(z, K, normalise=normalise)
+            ids2, w2 = vc.vcoll_moe_route(shifted(z), K, normalise=normalise)
+            assert torch.equal(ids, ids2) and torch.equal(w, w2), (E, K)
+            out = shifted(torch.zeros_like(z), 3)
+            vc.vcoll_moe_route_backward(shifted(z), shifted(ids), shifted(w), shifted(dw), normalise=normalise,
+                                        d_logits=out)
+            assert torch.equal(out, vc.vcoll_moe_route_backward(z, ids, w, dw, normalise=normalise)), (E, K)
+
+
+def test_route_backward_leaves_out_strange_ids(vc):
+    """Slots with ids outside [0, experts) add nothing, whatever their weight and gradient hold."""
+    z, z64 = logits(1, 4, 20, "f32", 2, False)
+    ids, w = vc.vcoll_moe_route(z, 3)
+    for normalise in (True, False):
+        bad_ids, bad_w = ids.clone(), w.clone()
+        dw = put(np.random.default_rng(3).normal(size=(1, 4, 3)))
+        bad_ids[0, 0, 1], bad_ids[0, 1, 0], bad_ids[0, 2] = -7, 20, 2 ** 31 - 1
+        gone = (bad_ids < 0) | (bad_ids >= 20)
+        if normalise:                                        # what is left of a token is a softmax of its own
+            live = put(np.where(get(gone), -np.inf, np.take_along_axis(z64, get(ids).astype(np.int64), 2)))
+            bad_w = live.softmax(-1).nan_to_num(0.0)
+        else:
+            bad_w = vc.vcoll_moe_route(z, 3, normalise=False)[1]
+        bad_w[gone] = float("nan")
+        dw[gone] = float("inf")
+        got = get(vc.vcoll_moe_route_backward(z, bad_ids, bad_w, dw, normalise=normalise)[0])
+        want = train.route_backward(z64[0], get(bad_ids[0]), get(dw[0]), normalise)
+        size = np.where(get(gone[0]), 0, np.abs(get(dw[0]))).max(axis=1)[:, None]
+        close(got, want, (2 * (2 * 50 + 40) + 16) * U * 2 * size + U * np.abs(want), str(normalise))
+
+
 def test_route_beyond_2_31_logits(vc):
     """The last tokens of a table of more than 2^31 logits."""
     import torch
@@ -418,6 +465,36 @@ def test_combine_of_unaligned_views(vc, name):
     assert all(torch.equal(x, y) for x, y in zip(de, de2))
     _, want, size = train.combine_weighted_backward(get(dy), [get(x) for x in e], slots, get(w), K)
     close(get(dw2), want, (H / 64 + 64) * U * size, "d_weights")
+
+
+def test_combine_of_lists_and_given_outputs(vc):
+    """Rank buffers as lists, results into given buffers; the refusals of overlaps."""
+    import torch
+    p, T, K, H = 3, 6, 3, 72
+    ts, slots, e, w, rng = experts_case(p, T, K, H, 2, "bf16", 6)
+    dy = put(rng.normal(size=(p, T, H)), "bf16")
+    want = vc.vcoll_moe_combine_weighted(e, ts, w, T, K)
+    want_e, want_w = vc.vcoll_moe_combine_weighted_backward(dy, e, ts, w, K)
+    lists = lambda x: [x[i].clone() for i in range(p)]                                        # noqa: E731
+    out = [torch.full((T, H), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(p)]
+    assert vc.vcoll_moe_combine_weighted(e, lists(ts), lists(w), T, K, out=out) is out
+    assert torch.equal(torch.stack(out), want)
+    dw = torch.full((p, T, K), 7.0, device="cuda")
+    de, dw2 = vc.vcoll_moe_combine_weighted_backward(lists(dy), e, lists(ts), lists(w), K, d_weights=dw)
+    assert dw2 is dw and torch.equal(dw, want_w) and all(torch.equal(a, b) for a, b in zip(de, want_e))
+    assert isinstance(vc.vcoll_moe_combine_weighted(e, lists(ts), w, T, K), list)
+    with pytest.raises(ValueError):
+        vc.vcoll_moe_combine_weighted_backward(dy, e, ts, w, K, d_expert_out=e)
+    with pytest.raises(ValueError):
+        vc.vcoll_moe_combine_weighted_backward(dy, e, ts, w, K, d_expert_out=[e[0][:1]] * p)
+    with pytest.raises(ValueError):
+        vc.vcoll_moe_combine_weighted_backward(dy, e, ts, w, K, d_weights=w)
+    with pytest.raises(ValueError):
+        vc.vcoll_moe_combine_weighted([dy[i] for i in range(p)], ts, w, T, K, out=dy)
+    empty = vc.vcoll_moe_combine_weighted([x[:0] for x in e], ts, w, T, K)
+    assert not bool(empty.any()), "no expert row at all: zeros"
+    none = vc.vcoll_moe_combine_weighted(e, ts[:, :0].contiguous(), w[:, :0].contiguous(), 0, K)
+    assert none.shape == (p, 0, H)
 
 
 def test_combine_rows_beyond_4_gib(vc):
