@@ -176,8 +176,10 @@ def vcoll_moe_route_backward(logits, ids, weights, d_weights, normalise: bool = 
 # expert sort
 
 
+@lru_cache(maxsize=1024)
 def vcoll_moe_sort_workspace(p: int, tokens: int, topk: int, experts_per_rank: int) -> int:
-    """Bytes of device workspace that vcoll_moe_sort needs for these sizes."""
+    """Bytes of device workspace that vcoll_moe_sort needs for these sizes (of
+    which alone it is a function)."""
     n = ctypes.c_int64()
     _check(_lib().vcoll_moe_sort_workspace(p, tokens, topk, experts_per_rank, ctypes.byref(n)),
            "vcoll_moe_sort_workspace")
