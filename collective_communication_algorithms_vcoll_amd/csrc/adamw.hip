@@ -262,14 +262,14 @@ __device__ __forceinline__ void adamw_tile(const AdamwArgs& a, const AdamwTensor
 
 template <class P, class G, int BITS>
 __global__ __launch_bounds__(kBlock) void adamw_kernel(const AdamwArgs a) {
-  int first = 0, last = a.count - 1;
-  while (first < last) {
-    const int mid = (first + last + 1) / 2;
-    if (a.t[mid].tile_start <= static_cast<int>(blockIdx.x)) first = mid;
-    else last = mid - 1;
-  }
-  const AdamwTensor& T = a.t[first];
-  const int64_t tile = static_cast<int64_t>(blockIdx.x - T.tile_start) * kAdamwTile - T.shift;
+  // the workgroup's tensor: the last that starts at or before it, found by all
+  // lanes at once (a binary search is a chain of loads from the argument
+  // buffer: 37 tensors of 6.55 M elements 35.2 us with it, 34.1 without)
+  const int lane = threadIdx.x % 64;
+  const bool begun = lane < kAdamwTensors && a.tile_start[lane] <= static_cast<int>(blockIdx.x);
+  const int at = __popcll(__ballot(begun)) - 1;
+  const AdamwTensor& T = a.t[at];
+  const int64_t tile = static_cast<int64_t>(static_cast<int>(blockIdx.x) - a.tile_start[at]) * kAdamwTile - T.shift;
   if (tile >= 0 && tile + kAdamwTile <= T.n) adamw_tile<P, G, BITS, true>(a, T, tile);
   else adamw_tile<P, G, BITS, false>(a, T, tile);
 }

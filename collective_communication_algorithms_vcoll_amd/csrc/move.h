@@ -108,7 +108,8 @@ hipError_t launch_broadcast(const BcastArgs& a, vcoll_dtype dtype, hipStream_t s
 hipError_t launch_all_to_all(const A2AArgs& a, int32_t tiles, hipStream_t stream);
 hipError_t launch_dispatch_fp8(const Fp8Args& a, int32_t tiles, hipStream_t stream);
 // Workgroups that share one tile of token rows, each copying one segment of
-// every row (1 when rows are short, FP8 or not 16-byte aligned).
+// every row (1 when rows are short (up to 4 KiB to push, 1 KiB to pull), FP8
+// or not 16-byte aligned).
 int32_t push_segments(int64_t row_bytes, bool fp8, bool vec);
 int32_t pull_segments(int64_t row_bytes, bool vec);
 hipError_t launch_dispatch_push(const PushArgs& a, bool fp8, hipStream_t stream);

@@ -335,11 +335,12 @@ __global__ __launch_bounds__(kBlock) void dispatch_fp8_kernel(const Fp8Args a) {
 constexpr int kPushUnroll = 4;     // 16-byte vectors in flight per thread (a 7168 bf16 row is 3.5)
 constexpr int kPushFp8Block = 512;  // threads per workgroup of the FP8 token-major dispatch
 
-// bf16 token rows longer than this many 16-byte vectors are cut into
-// segments of it, one per one-wave workgroup (the workgroups of one token
+// Token rows longer than kPushRowsVec 16-byte vectors are cut into segments
+// of kPushSegVec, one per one-wave workgroup (the workgroups of one token
 // then write its copies in parallel): on the 7168-element MoE workload,
 // seven 2 KiB segments took the dispatch from 836 to 775 us on MI355X.
 constexpr int kPushSegVec = 128;
+constexpr int kPushRowsVec = 256;
 
 template <bool FP8, int BS>
 __global__ __launch_bounds__(BS) void dispatch_push_kernel(const PushArgs a) {
@@ -405,14 +406,17 @@ __global__ __launch_bounds__(BS) void dispatch_push_kernel(const PushArgs a) {
   }
 }
 
-// Rows of up to kPushSegVec vectors, and rows or buffers off a 16-byte
+// Rows of up to kPushRowsVec vectors, and rows or buffers off a 16-byte
 // boundary: one thread per 16 bytes of a token row, tokens side by side in a
 // workgroup, so that many short rows are in flight at once; the last thread
 // of a row copies the bytes past its last whole vector in 2-byte words.
 // Against 16 KiB of rows per workgroup, one token after the other (unaligned
 // ones two bytes at a time), on MI355X: 2 x 295 tokens of 144 bf16 to 10
 // experts 144 -> 5.5 us, 8 x 4096 of 512 bf16 to 8 experts 105 -> 55 us (5.5
-// TB/s), of 1024 155 -> 116 us, 8 x 1024 of 2639 bf16 306 -> 121 us.
+// TB/s), of 1024 155 -> 116 us, 8 x 1024 of 2639 bf16 306 -> 121 us. Against
+// segments, 16 x 1682 of 1168 bf16 to 9 experts 205 -> 157 us, 8 x 4096 of
+// 2048 to 8 251 -> 236, to 2 66 -> 69; beyond 4 KiB the two are within 5 %
+// either way.
 __global__ __launch_bounds__(kBlock) void dispatch_rows_kernel(const PushArgs a) {
   const int i = blockIdx.y;
   const uint32_t lanes = static_cast<uint32_t>((a.row_bytes + 15) / 16);
@@ -585,7 +589,7 @@ hipError_t launch_dispatch_fp8(const Fp8Args& a, int32_t tiles, hipStream_t stre
 int32_t push_segments(int64_t row_bytes, bool fp8, bool vec) {
   if (fp8 || !vec) return 1;
   const int64_t nvec = row_bytes / 16;
-  return static_cast<int32_t>(nvec > kPushSegVec ? (nvec + kPushSegVec - 1) / kPushSegVec : 1);
+  return static_cast<int32_t>(nvec > kPushRowsVec ? (nvec + kPushSegVec - 1) / kPushSegVec : 1);
 }
 
 int32_t pull_segments(int64_t row_bytes, bool vec) {

@@ -83,7 +83,7 @@ struct WeightedBackwardArgs {
 };
 static_assert(sizeof(WeightedBackwardArgs) <= 4096, "kernel arguments are limited to 4 KiB");
 
-constexpr int kAdamwTensors = 48;    // tensors described per launch
+constexpr int kAdamwTensors = 48;    // tensors described per launch, at most one per lane
 constexpr int kAdamwGroup = 128;     // elements per scale of an 8-bit state
 constexpr int kAdamwTile = 1024;     // elements per workgroup, a multiple of the group
 
@@ -96,14 +96,13 @@ struct AdamwTensor {
   void* exp_avg_sq;
   float* exp_avg_scale;              // null with float32 states
   float* exp_avg_sq_scale;
-  int32_t tile_start;                // first workgroup of this tensor
   uint32_t key;                      // of the tensor's random rounding
   int32_t shift;                     // elements before the tensor in its first tile
-  int32_t pad;
 };
 
 struct AdamwArgs {
   AdamwTensor t[kAdamwTensors];
+  int32_t tile_start[kAdamwTensors]; // first workgroup of every tensor; past the last tensor INT32_MAX
   float beta1, one_minus_beta1, beta2, one_minus_beta2;
   float grad_scale;
   float decay;                       // 1 - lr * weight_decay

@@ -310,8 +310,10 @@ vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dty
                                                   static_cast<hipStream_t>(stream)));
     a.count = 0;
     tiles = 0;
+    std::fill(a.tile_start, a.tile_start + kAdamwTensors, INT32_MAX);
     return st;
   };
+  std::fill(a.tile_start, a.tile_start + kAdamwTensors, INT32_MAX);
   for (int k = 0; k < count; ++k) {
     const vcoll_adamw_tensor& t = tensors[k];
     if (t.n == 0) continue;
@@ -324,6 +326,7 @@ vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dty
       const vcoll_status st = run();
       if (st != VCOLL_OK) return st;
     }
+    a.tile_start[a.count] = static_cast<int32_t>(tiles);
     AdamwTensor& d = a.t[a.count++];
     d.n = t.n;
     d.param = t.param;
@@ -333,7 +336,6 @@ vcoll_status vcoll_adamw(int count, const vcoll_adamw_tensor* tensors, vcoll_dty
     d.exp_avg_sq = t.exp_avg_sq;
     d.exp_avg_scale = t.exp_avg_scale;
     d.exp_avg_sq_scale = t.exp_avg_sq_scale;
-    d.tile_start = static_cast<int32_t>(tiles);
     d.shift = static_cast<int32_t>(shift);
     d.key = mix32(first + 0x9E3779B9u * static_cast<uint32_t>(k));
     tiles += more;

@@ -56,11 +56,12 @@ hipError_t launch_adamw(const AdamwArgs& a, int32_t tiles, vcoll_dtype, vcoll_dt
   CHECK(a.count >= 1 && a.count <= kAdamwTensors);
   int64_t at = 0;
   for (int k = 0; k < a.count; ++k) {
-    CHECK(a.t[k].tile_start == at && a.t[k].n > 0);
+    CHECK(a.tile_start[k] == at && a.t[k].n > 0);
     CHECK(a.t[k].shift >= 0 && a.t[k].shift < 32);
     at += (a.t[k].n + a.t[k].shift + kAdamwTile - 1) / kAdamwTile;
     g_seen.push_back(a.t[k].param);
   }
+  for (int k = a.count; k < kAdamwTensors; ++k) CHECK(a.tile_start[k] == INT32_MAX);
   CHECK(at == tiles);
   g_tiles += tiles;
   return hipSuccess;
