@@ -267,7 +267,7 @@ hipError_t launch_weighted_v(WeightedArgs a, hipStream_t stream) {
 template <int D, int Q>
 hipError_t launch_weighted_q(const WeightedArgs& a, hipStream_t stream) {
   const int64_t row_bytes = a.hidden * sizeof(typename Storage<D>::elem);
-  if constexpr (Q == 2) {
+  if constexpr (Q <= 2) {
     if (row_bytes > 2 * kSegment) return launch_weighted_v<D, Q, 4>(a, stream);
     if (row_bytes > kSegment) return launch_weighted_v<D, Q, 2>(a, stream);
   }
@@ -282,18 +282,19 @@ hipError_t launch_weighted_backward_q(const WeightedBackwardArgs& a, hipStream_t
   return launch(weighted_backward_kernel<D, Q>, grid, block, a, stream);
 }
 
-// Rows in flight: the even number up to 8 that wastes the fewest places on a
-// token's topk rows (7 and 8 take 8, 6 takes 6, 10 takes 6 twice).
+// Rows in flight: a token's topk rows in as few steps of up to 8 as they
+// need, as even as they get (9 and 10 take 6 twice, 20 takes 8 three times).
+// An idle place costs little (3 rows in steps of 4 150.9 us, of 3 149.8; 7 in
+// steps of 8 182, of 7 185), so only one row has a step of its own odd size
+// (its gradient of 2048 bf16 for 8 x 4096 tokens 76 us, 86 in a step of 2).
 template <class F>
 hipError_t by_rows(int topk, F&& run) {
   using std::integral_constant;
-  int best = 8;
-  for (int q : {6, 4, 2})
-    if ((topk + q - 1) / q * q < (topk + best - 1) / best * best) best = q;
-  if (topk > 8 && best < 6) best = 6;               // long lists: fewer steps rather than fewer idle places
-  if (best == 2) return run(integral_constant<int, 2>{});
-  if (best == 4) return run(integral_constant<int, 4>{});
-  if (best == 6) return run(integral_constant<int, 6>{});
+  const int steps = (topk + 7) / 8, rows = (topk + steps - 1) / steps;
+  if (rows == 1) return run(integral_constant<int, 1>{});
+  if (rows <= 2) return run(integral_constant<int, 2>{});
+  if (rows <= 4) return run(integral_constant<int, 4>{});
+  if (rows <= 6) return run(integral_constant<int, 6>{});
   return run(integral_constant<int, 8>{});
 }
 
