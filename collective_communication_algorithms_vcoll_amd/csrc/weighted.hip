@@ -24,7 +24,6 @@ namespace {
 
 using namespace dev;
 
-
 // Expert rows are read once and written once, so both stream past the caches.
 // On MI355X, with the rows of 8 x 4096 tokens x 8 experts x 7168 bf16 (3.76
 // GB) read and the 0.47 GB of outputs written, the combine takes 716 us (5.9
@@ -163,15 +162,16 @@ __device__ __forceinline__ float wave_sums8(const float* x, int lane) {
   float y[4], z[2];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float keep = lane & 4 ? x[q + 4] : x[q], give = lane & 4 ? x[q] : x[q + 4];
-    y[q] = keep + lane_xor<4>(give);
+    const float low = x[q], high = x[q + 4];
+    y[q] = (lane & 4 ? high : low) + lane_xor<4>(lane & 4 ? low : high);
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const float keep = lane & 2 ? y[q + 2] : y[q], give = lane & 2 ? y[q] : y[q + 2];
-    z[q] = keep + lane_xor<2>(give);
+    const float low = y[q], high = y[q + 2];
+    z[q] = (lane & 2 ? high : low) + lane_xor<2>(lane & 2 ? low : high);
   }
-  float s = (lane & 1 ? z[1] : z[0]) + lane_xor<1>(lane & 1 ? z[0] : z[1]);
+  const float low = z[0], high = z[1];
+  float s = (lane & 1 ? high : low) + lane_xor<1>(lane & 1 ? low : high);
   s += lane_xor<8>(s);
   s += lane_xor<16>(s);
   return s + __shfl_xor(s, 32);
